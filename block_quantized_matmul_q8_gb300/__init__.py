@@ -32,7 +32,9 @@ EXPORTS = ("qmm_status_string", "qmm_q8_1_bytes", "qmm_row_bytes", "qmm_workspac
            "qmm_mul_mat_id_slot", "qmm_workspace_bytes_glu", "qmm_mul_mat_glu", "qmm_gemv_ring_stages",
            "qmm_repack_glu", "qmm_mul_mat_glu_packed", "qmm_workspace_bytes_f32_host", "qmm_mul_mat_f32_host",
            "qmm_get_device_status", "qmm_set_test_fault", "qmm_aligned_row_bytes", "qmm_repack_aligned",
-           "qmm_workspace_bytes_aligned", "qmm_mul_mat_aligned", "qmm_workspace_bytes_id_glu", "qmm_mul_mat_id_glu")
+           "qmm_workspace_bytes_aligned", "qmm_mul_mat_aligned", "qmm_workspace_bytes_id_glu", "qmm_mul_mat_id_glu",
+           "qmm_qk_norm_rope", "qmm_workspace_bytes_attn_prompt", "qmm_attn_prompt",
+           "qmm_workspace_bytes_attn_decode", "qmm_attn_decode")
 
 
 class QMMError(RuntimeError):
@@ -50,6 +52,13 @@ class GemmPlan(ctypes.Structure):
     def as_dict(self):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
+
+class Heads(ctypes.Structure):
+    """A [tokens][heads][head_dim] view (qmm_heads): data pointer and strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 30}
 
 _lib = None
 
@@ -129,6 +138,20 @@ def lib():
     L.qmm_workspace_bytes_f32.argtypes = [ctypes.c_int, I64, I64, I64]
     L.qmm_mul_mat_f32.restype = ctypes.c_int
     L.qmm_mul_mat_f32.argtypes = [P, ctypes.c_int, I64, I64, P, I64, P, P, SZ, P]
+    HP, F32 = ctypes.POINTER(Heads), ctypes.c_float
+    L.qmm_qk_norm_rope.restype = ctypes.c_int
+    L.qmm_qk_norm_rope.argtypes = [HP, HP, HP, ctypes.c_int, I64, I64, I64, I64, P, P, F32, P, P, I64, ctypes.c_int,
+                                   HP, HP, HP, ctypes.c_int, P]
+    L.qmm_workspace_bytes_attn_prompt.restype = SZ
+    L.qmm_workspace_bytes_attn_prompt.argtypes = [I64] * 6
+    L.qmm_attn_prompt.restype = ctypes.c_int
+    L.qmm_attn_prompt.argtypes = [HP, HP, HP, ctypes.c_int, I64, I64, I64, I64, I64, P, P, I64, ctypes.c_int, F32, HP,
+                                  P, P, SZ, P]
+    L.qmm_workspace_bytes_attn_decode.restype = SZ
+    L.qmm_workspace_bytes_attn_decode.argtypes = [I64] * 6
+    L.qmm_attn_decode.restype = ctypes.c_int
+    L.qmm_attn_decode.argtypes = [HP, HP, HP, I64, I64, P, I64, I64, HP, HP, I64, ctypes.c_int, I64, I64, I64, F32, HP,
+                                  P, P, SZ, P]
     _lib = L
     return L
 
@@ -427,6 +450,156 @@ def qmm_read_device_status(workspace: torch.Tensor, stream=None) -> int:
 def qmm_get_device_status(workspace: torch.Tensor, stream=None) -> int:
     """The status word of the last mul_mat_id on this workspace (synchronises the stream)."""
     return int(lib().qmm_get_device_status(_ptr(workspace), _stream(stream)))
+
+
+def _heads(t: torch.Tensor, name: str, shape=None, dtype=None) -> Heads:
+    """The qmm_heads of a CUDA tensor whose last three dimensions are [tokens, heads, head_dim]."""
+    if not t.is_cuda:
+        raise QMMError(1, f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise QMMError(3, f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise QMMError(2, f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise QMMError(1, f"{name}: the elements of a head must be contiguous")
+    return Heads(t.data_ptr(), st[-3], st[-2])
+
+
+def _small(t, name, dtype, numel):
+    """A contiguous CUDA tensor of `numel` elements (or None), as a pointer."""
+    if t is None:
+        return None
+    _dev(t, name, dtype)
+    if t.numel() != numel:
+        raise QMMError(2, f"{name} must have {numel} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _scratch(need, workspace, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    return _dev(workspace, "workspace")
+
+
+def _on_stream(stream, *made):
+    """The stream's handle; tensors that a call made for itself are kept until that stream is done with them."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    for t in made:
+        t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def qmm_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None, positions: torch.Tensor | None,
+                     inv_freq: torch.Tensor | None, w_q: torch.Tensor | None = None, w_k: torch.Tensor | None = None,
+                     eps: float = 1e-6, interleaved: bool = False, out_dtype=torch.bfloat16,
+                     q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                     v_out: torch.Tensor | None = None, stream=None):
+    """RMS norm and rotation of the heads of q [m, heads, d] and k [m, kv_heads, d], rounded to
+    out_dtype together with v; returns (q_out, k_out, v_out).  inv_freq: fp32 [rotary_dim / 2]
+    or None for no rotation.  Views of a fused projection's rows are taken as they are, and
+    outputs may be views of a cache."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise QMMError(2, "q and k must be [tokens, heads, head_dim]")
+    m, hq, d = q.shape
+    hk = k.shape[1]
+    if q_out is None:
+        q_out = torch.empty((m, hq, d), dtype=out_dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((m, hk, d), dtype=out_dtype, device=q.device)
+    if v is not None and v_out is None:
+        v_out = torch.empty((m, hk, d), dtype=out_dtype, device=q.device)
+    if q.dtype not in FLOATS or out_dtype not in FLOATS:
+        raise QMMError(3, "q must be fp32, fp16 or bf16")
+    kv = (m, hk, d)
+    args = [_heads(q, "q"), _heads(k, "k", kv, q.dtype), None if v is None else _heads(v, "v", kv, q.dtype),
+            _heads(q_out, "q_out", q.shape, out_dtype), _heads(k_out, "k_out", kv, out_dtype),
+            None if v is None else _heads(v_out, "v_out", kv, out_dtype)]
+    rotary = 0 if inv_freq is None else 2 * inv_freq.numel()
+    _check(lib().qmm_qk_norm_rope(args[0], args[1], args[2], FLOATS[q.dtype], m, hq, hk, d,
+                                  _small(w_q, "w_q", torch.float32, d), _small(w_k, "w_k", torch.float32, d), eps,
+                                  _small(positions, "positions", torch.int32, m),
+                                  _small(inv_freq, "inv_freq", torch.float32, rotary // 2), rotary, int(interleaved),
+                                  args[3], args[4], args[5], FLOATS[out_dtype],
+                                  _on_stream(stream, q_out, k_out, *(() if v is None else (v_out,)))),
+           "qmm_qk_norm_rope")
+    return q_out, k_out, v_out
+
+
+def qmm_workspace_bytes_attn_prompt(tokens_q: int, tokens_k: int, n_seqs: int, heads_q: int, heads_kv: int,
+                                    head_dim: int) -> int:
+    return lib().qmm_workspace_bytes_attn_prompt(tokens_q, tokens_k, n_seqs, heads_q, heads_kv, head_dim)
+
+
+def qmm_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                    cu_k: torch.Tensor | None = None, causal: bool = True, scale: float | None = None,
+                    out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention over packed sequences: q [tokens_q, heads, d], k and v [tokens_k, kv_heads, d] in fp16
+    or bf16, cu_q and cu_k int32 [n_seqs + 1] row bounds (cu_k None: the same as cu_q)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise QMMError(2, "q and k must be [tokens, heads, head_dim]")
+    (tq, hq, d), (tk, hk, _) = q.shape, k.shape
+    if q.dtype not in FLOATS:
+        raise QMMError(3, "q must be fp16 or bf16")
+    made = out is None
+    if made:
+        out = torch.empty((tq, hq, d), dtype=q.dtype, device=q.device)
+    n = cu_q.numel() - 1
+    cu_k = cu_q if cu_k is None else cu_k
+    ws = _scratch(qmm_workspace_bytes_attn_prompt(tq, tk, n, hq, hk, d), workspace, q.device)
+    _check(lib().qmm_attn_prompt(_heads(q, "q"), _heads(k, "k", (tk, hk, d), q.dtype),
+                                 _heads(v, "v", (tk, hk, d), q.dtype), FLOATS[q.dtype], tq, tk, hq, hk, d,
+                                 _small(cu_q, "cu_q", torch.int32, n + 1), _small(cu_k, "cu_k", torch.int32, n + 1), n,
+                                 int(causal), d ** -0.5 if scale is None else scale,
+                                 _heads(out, "out", q.shape, q.dtype), _small(lse, "lse", torch.float32, tq * hq),
+                                 ws.data_ptr(), ws.numel() * ws.element_size(),
+                                 _on_stream(stream, *((ws,) if workspace is None else ()), *((out,) if made else ()))),
+           "qmm_attn_prompt")
+    return out
+
+
+def qmm_workspace_bytes_attn_decode(batch: int, room: int, prefix_len: int, heads_q: int, heads_kv: int,
+                                    head_dim: int) -> int:
+    return lib().qmm_workspace_bytes_attn_decode(batch, room, prefix_len, heads_q, heads_kv, head_dim)
+
+
+def qmm_attn_decode(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | None, lens: torch.Tensor | None,
+                    prefix_k: torch.Tensor | None = None, prefix_v: torch.Tensor | None = None,
+                    scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One query token for each request, q [batch, heads, d], over prefix_k and prefix_v [prefix_len, kv_heads, d]
+    that all requests share and the caches k and v [batch, room, kv_heads, d] with lens int32 [batch]."""
+    if q.dim() != 3 or (k is None and prefix_k is None):
+        raise QMMError(2, "q must be [batch, heads, head_dim], with caches or a prefix")
+    b, hq, d = q.shape
+    if q.dtype not in FLOATS:
+        raise QMMError(3, "q must be fp16 or bf16")
+    if k is not None and k.dim() != 4:
+        raise QMMError(2, "k must be [batch, room, kv_heads, head_dim]")
+    hk = (k if k is not None else prefix_k).shape[-2]
+    room = 0 if k is None else k.shape[1]
+    p = 0 if prefix_k is None else prefix_k.shape[0]
+    kh = vh = pk = pv = None
+    if k is not None:
+        kh, vh = (_heads(x, n, (b, room, hk, d), q.dtype) for x, n in ((k, "k"), (v, "v")))
+    if prefix_k is not None:
+        pk, pv = (_heads(x, n, (p, hk, d), q.dtype) for x, n in ((prefix_k, "prefix_k"), (prefix_v, "prefix_v")))
+    made = out is None
+    if made:
+        out = torch.empty((b, hq, d), dtype=q.dtype, device=q.device)
+    ws = _scratch(qmm_workspace_bytes_attn_decode(b, room, p, hq, hk, d), workspace, q.device)
+    _check(lib().qmm_attn_decode(_heads(q, "q"), kh, vh, 0 if k is None else k.stride(0),
+                                 0 if k is None else v.stride(0), _small(lens, "lens", torch.int32, b), b, room, pk, pv,
+                                 p, FLOATS[q.dtype], hq, hk, d, d ** -0.5 if scale is None else scale,
+                                 _heads(out, "out", q.shape, q.dtype), _small(lse, "lse", torch.float32, b * hq),
+                                 ws.data_ptr(), ws.numel() * ws.element_size(),
+                                 _on_stream(stream, *((ws,) if workspace is None else ()), *((out,) if made else ()))),
+           "qmm_attn_decode")
+    return out
 
 
 def qmm_tile_efficiency_percent(ntiles: int, nsm: int) -> int:

@@ -346,7 +346,7 @@ QMM_API qmm_status qmm_mul_mat_id_noalloc(const void *W_experts, qmm_type t, int
 /* Size in bytes of the fixed scratch array used by qmm_mul_mat_id_noalloc. */
 QMM_API size_t qmm_noalloc_scratch_bytes(void);
 
-/* Copy the device status word of the last qmm_mul_mat_id on this workspace to
+/* Copy the device status word of the last qmm_mul_mat_id (or attention call) on this workspace to
  * *status (QMM_OK, QMM_ERR_IDS or QMM_ERR_DEVICE).  This call synchronises
  * `stream`.  Returns QMM_ERR_CUDA if the copy fails. */
 QMM_API qmm_status qmm_read_device_status(const void *workspace, int32_t *status, void *stream);
@@ -358,6 +358,101 @@ QMM_API qmm_status qmm_read_device_status(const void *workspace, int32_t *status
  * the writer).  QMM_ERR_ARG for a NULL workspace, QMM_ERR_CUDA if the read fails, so a
  * caller that must tell a failed read from a device error uses qmm_read_device_status. */
 QMM_API qmm_status qmm_get_device_status(const void *workspace, void *stream);
+
+/* ------------------------------------------------------------------ attention
+ * Between the qkv projection and the output projection of a decoder layer: the norm and
+ * rotation of queries and keys, attention over packed prompts, and attention of a
+ * decoding batch (interfaces of this library; the pages have no counterpart).
+ * Heads are 16-bit (what a key/value cache holds); scores, softmax statistics and sums
+ * are fp32. */
+
+/* Element types of the attention calls. */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 30 } qmm_float;
+
+/* A [tokens][heads][head_dim] view of device memory: element (t, h, d) is
+ * data[t * token_stride + h * head_stride + d], strides in elements.  data and both
+ * strides are whole 16-byte units (QMM_ERR_ALIGN) and a stride is at least head_dim
+ * (QMM_ERR_SHAPE), except one that is never taken (one token, one head).  A slice of a fused
+ * projection's output and a cache are such views. */
+typedef struct {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+} qmm_heads;
+
+/*
+ * RMS norm of every query and key head, rotation by position, and rounding to 16 bits in
+ * one pass; the values are rounded in the same pass:
+ *   n[d] = x[d] * w[d] / sqrt(mean_d(x[d]^2) + eps)        (w == NULL: n = x)
+ *   the pairs (a, b) = (n[i], n[i + rotary_dim/2]), or (n[2i], n[2i+1]) when interleaved,
+ *   i < rotary_dim/2, turn by the angle positions[t] * inv_freq[i]:
+ *   (a cos - b sin, b cos + a sin); the other elements stay.
+ * The angle is reduced in fp64, so it is as exact at position 2^31 - 1 as at 1.
+ *   q, k, v   : in_type (QMM_F32, QMM_F16 or QMM_BF16) [m] tokens of heads_q, heads_kv and
+ *               heads_kv heads; v (with v_out) may be NULL.
+ *   w_q, w_k  : fp32 [head_dim], or NULL for no norm.
+ *   positions : int32 [m]; inv_freq : fp32 [rotary_dim/2]; unused when rotary_dim == 0.
+ *   q_out, k_out, v_out : out_type (QMM_F16 or QMM_BF16); every element is written.  An output
+ *               may be its own input (same data, strides and type); other overlaps are not allowed.
+ * head_dim: a multiple of 8, 8..128; rotary_dim: a multiple of 8, 0..head_dim.
+ */
+QMM_API qmm_status qmm_qk_norm_rope(const qmm_heads *q, const qmm_heads *k, const qmm_heads *v, qmm_float in_type,
+                                    int64_t m, int64_t heads_q, int64_t heads_kv, int64_t head_dim, const float *w_q,
+                                    const float *w_k, float eps, const int32_t *positions, const float *inv_freq,
+                                    int64_t rotary_dim, int interleaved, const qmm_heads *q_out,
+                                    const qmm_heads *k_out, const qmm_heads *v_out, qmm_float out_type, void *stream);
+
+/*
+ * Attention over whole prompts, packed one after another:
+ *   out[t][h] = sum_j p_j v[j][h / G],  p = softmax_j(scale * q[t][h] . k[j][h / G]),
+ *   G = heads_q / heads_kv, over the keys j of t's own sequence.
+ *   cu_q, cu_k : int32 [n_seqs + 1] on the device: sequence s holds the query rows
+ *                [cu_q[s], cu_q[s+1]) and the key rows [cu_k[s], cu_k[s+1]), both
+ *                non-decreasing; either may be empty.  The host never reads them.  Bounds
+ *                outside [0, tokens] are taken as the nearest of the two.
+ *   causal     : nonzero: the queries are the last ones of the keys, query i of a sequence of
+ *                lq queries and lk keys sees the keys j <= i + (lk - lq).
+ *   q, out     : type t [tokens_q] tokens of heads_q heads; k, v: [tokens_k] tokens of heads_kv.
+ *   lse        : fp32 [tokens_q][heads_q], the log of the softmax's denominator, or NULL.
+ *   workspace  : qmm_workspace_bytes_attn_prompt(...) bytes, 256-byte aligned; it also holds
+ *                the status word of qmm_read_device_status.
+ * A row that sees no key gives zeros (lse -infinity).  A key that a row does not see has no
+ * influence on it, whatever its k and v hold (infinities and NaN included).  Query rows
+ * outside every sequence are not written.  heads_q is a multiple of heads_kv, at most 128
+ * times it; head_dim a multiple of 8, 8..128.
+ */
+QMM_API size_t qmm_workspace_bytes_attn_prompt(int64_t tokens_q, int64_t tokens_k, int64_t n_seqs, int64_t heads_q,
+                                               int64_t heads_kv, int64_t head_dim);
+QMM_API qmm_status qmm_attn_prompt(const qmm_heads *q, const qmm_heads *k, const qmm_heads *v, qmm_float t,
+                                   int64_t tokens_q, int64_t tokens_k, int64_t heads_q, int64_t heads_kv,
+                                   int64_t head_dim, const int32_t *cu_q, const int32_t *cu_k, int64_t n_seqs,
+                                   int causal, float scale, const qmm_heads *out, float *lse, void *workspace,
+                                   size_t ws_bytes, void *stream);
+
+/*
+ * Attention of a decoding batch: one query token for each request, over a prefix that all
+ * requests share (read once for all of them) followed by the request's own cache:
+ *   out[b][h] = softmax over {prefix rows, cache rows j < lens[b]} as in qmm_attn_prompt.
+ *   q, out : type t [batch] tokens of heads_q heads.
+ *   k, v   : the caches, [batch][room] tokens of heads_kv heads; request b's cache starts
+ *            k_batch_stride (v_batch_stride) elements after request b - 1's, whole 16-byte units.
+ *   lens   : int32 [batch] on the device, taken as the nearest value of [0, room].
+ *   prefix_k, prefix_v : [prefix_len] tokens of heads_kv heads; prefix_len == 0: none (may be
+ *            NULL), which is the single-token form of attention over separate caches.
+ *   room may be 0 (then k, v may be NULL).  lse: fp32 [batch][heads_q] or NULL.
+ *   workspace : qmm_workspace_bytes_attn_decode(...) bytes, 256-byte aligned; it also holds the
+ *            status word of qmm_read_device_status.
+ * Cache rows from lens[b] on have no influence, whatever they hold.  A request without any
+ * key gives zeros (lse -infinity).  Heads and sizes as for qmm_attn_prompt.
+ */
+QMM_API size_t qmm_workspace_bytes_attn_decode(int64_t batch, int64_t room, int64_t prefix_len, int64_t heads_q,
+                                               int64_t heads_kv, int64_t head_dim);
+QMM_API qmm_status qmm_attn_decode(const qmm_heads *q, const qmm_heads *k, const qmm_heads *v,
+                                   int64_t k_batch_stride, int64_t v_batch_stride, const int32_t *lens, int64_t batch,
+                                   int64_t room, const qmm_heads *prefix_k, const qmm_heads *prefix_v,
+                                   int64_t prefix_len, qmm_float t, int64_t heads_q, int64_t heads_kv,
+                                   int64_t head_dim, float scale, const qmm_heads *out, float *lse, void *workspace,
+                                   size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ host-side planning
  * These functions run on the host only and never touch a GPU. */
