@@ -1,4 +1,4 @@
-// qmm_attn.cu -- attention of packed prompts and of a decoding batch.
+// qmm_attn.cu -- attention of a decoding batch.
 //
 //   out = sum_j p_j v_j,  p = softmax_j(scale q.k_j) over the keys that the row sees.
 //
@@ -100,31 +100,6 @@ template <typename T> __device__ __forceinline__ void finish(const Row &s, T *ou
 
 __device__ __forceinline__ float4 scaled(float4 q, float f) { return make_float4(q.x * f, q.y * f, q.z * f, q.w * f); }
 
-template <typename T> __global__ void __launch_bounds__(kRowWarps * 32) prompt_rows_kernel(const PromptArgs a) {
-    const int lane = threadIdx.x & 31, h = blockIdx.y;
-    const int64_t t = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-    if (t >= a.tokens_q) return;
-    const bool live = 4 * lane < a.shape.d;
-    auto bound = [](int32_t x, int64_t most) { return min(max(int64_t(x), int64_t(0)), most); };
-    for (int64_t s = 0; s < a.n_seqs; ++s) {
-        const int64_t q0 = bound(a.cu_q[s], a.tokens_q), q1 = bound(a.cu_q[s + 1], a.tokens_q);
-        if (t < q0 || t >= q1) continue;
-        const int64_t k0 = bound(a.cu_k[s], a.tokens_k), k1 = max(bound(a.cu_k[s + 1], a.tokens_k), k0);
-        int64_t n = k1 - k0;
-        if (a.causal) n = min(n, max(t - q0 + 1 + n - (q1 - q0), int64_t(0)));
-        const int hk = h / (a.shape.hq / a.shape.hk);
-        const float4 q =
-            live ? scaled(load4(static_cast<const T *>(a.q) + t * a.sq.t + h * a.sq.h + 4 * lane), a.scale)
-                 : make_float4(0.f, 0.f, 0.f, 0.f);
-        Row row;
-        take_keys(row, q, static_cast<const T *>(a.k) + k0 * a.sk.t + hk * a.sk.h + 4 * lane,
-                  static_cast<const T *>(a.v) + k0 * a.sv.t + hk * a.sv.h + 4 * lane, a.sk.t, a.sv.t, n, live);
-        finish(row, static_cast<T *>(a.out) + t * a.so.t + h * a.so.h + 4 * lane,
-               a.lse ? a.lse + t * a.shape.hq + h : nullptr, lane, live);
-        return;
-    }
-}
-
 template <typename T> __global__ void __launch_bounds__(kRowWarps * 32) decode_rows_kernel(const DecodeArgs a) {
     const int lane = threadIdx.x & 31, h = blockIdx.y;
     const int64_t b = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
@@ -147,17 +122,7 @@ template <typename T> __global__ void __launch_bounds__(kRowWarps * 32) decode_r
 
 }  // namespace
 
-size_t attn_prompt_workspace_bytes(const PromptArgs &) { return 256; }
 size_t attn_decode_workspace_bytes(const DecodeArgs &) { return 256; }
-
-cudaError_t launch_attn_prompt(const PromptArgs &a, qmm_float t, void *ws, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(ws, 0, 16, st);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((a.tokens_q + kRowWarps - 1) / kRowWarps), (unsigned)a.shape.hq);
-    if (t == QMM_F16) prompt_rows_kernel<__half><<<grid, kRowWarps * 32, 0, st>>>(a);
-    else prompt_rows_kernel<__nv_bfloat16><<<grid, kRowWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_attn_decode(const DecodeArgs &a, qmm_float t, void *ws, cudaStream_t st) {
     cudaError_t e = cudaMemsetAsync(ws, 0, 16, st);

@@ -1,0 +1,690 @@
+// qmm_attn_tc.cu -- attention on the tensor cores: packed prompts, and a batch's queries over
+// a prefix that all its requests share.
+//
+//   out = sum_j p_j v_j,  p = softmax_j(scale q.k_j) over the keys j that a row sees.
+//
+// One CTA takes 2 x 128 rows of one key/value head: the query heads that share it are rows of
+// the same tile (row = token * G + g), so a tile of K and V is read once for all of them.  It
+// walks the keys in tiles of 128 with the running maximum and sum of a softmax:
+//   S_i = Q_i K_j^T (tcgen05, fp32 in tensor memory)   -> P_i = exp2(scale' (S_i - top)), rounded
+//   to the inputs' type into the columns of S_i         -> O_i += P_i V_j (A from tensor memory).
+// While the softmax threads of one half (128 threads, one row each) work, the tensor cores run
+// the other half's two products.  A row's maximum is only moved when it grows by more than 2^8
+// (weights then stay below 256, exact in the fp32 sums), so O_i is rarely rescaled.
+//
+// Warps: 0-3 and 4-7 softmax of half 0 and 1, 8 TMA copies, 9 MMA issue (10 and 11 only fill up
+// their warpgroup, which gives its registers to the softmax ones).
+// Bounds: at large sizes the tensor pipe and the exponentials (128 x 128 per 2 x 128x128xD
+// products) take about the same time; at small ones the start of the CTA (copy latency).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "qmm_attn.h"
+#include "qmm_internal.h"
+#include "qmm_tc_common.cuh"
+#include "qmm_tc_ptx.cuh"
+
+namespace qmm {
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kRows = 128;    // rows of one half
+constexpr int kKeys = 128;    // keys of one tile
+constexpr int kTcThreads = 384;  // 168 registers each at launch: 64512 in all
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;  // 256 * 224 + 128 * 56 = 64512
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;  // how far (in powers of two) a row's scores may pass its maximum
+
+// Shared-memory plan for a padded head size DP: Q_0, Q_1, then a ring of K and V tiles.  A tile
+// is DP/64 blocks of 128 rows x 128 bytes, 128-byte swizzled.
+template <int DP> struct Plan {
+    static constexpr int kTile = kRows * DP * 2;
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr size_t kBytes = size_t(2 + kStages) * kTile + 1024;
+};
+
+struct TcArgs {
+    CUtensorMap q, k, v;
+    void *out;              // direct output (splits == 1)
+    float *lse;             // [tokens][hq] natural log, or nullptr (splits == 1)
+    float *part;            // splits > 1: normalised fp32 partial rows [split][tokens * hq][d]
+    float *part_lse;        // their log2 denominators [split][tokens * hq]
+    const void *v_data;     // V again, for the rare rows with non-finite values
+    HeadStrides so, sv;
+    HeadShape shape;
+    const int32_t *cu_q, *cu_k;  // nullptr: one sequence of tokens_q queries and tokens_k keys
+    int64_t n_seqs, tokens_q, tokens_k;
+    int group, per_half;    // query heads of a kv head, tokens of one half
+    int causal, splits;
+    float scale_log2;       // |scale| * log2(e)
+    uint32_t idesc_qk, idesc_pv;
+    int *status;
+};
+
+// What a CTA works on: query tokens [t0, t0 + tokens) of the sequence's lq (row q0 first), its
+// keys [k0, k0 + lk).
+struct Item {
+    int q0, lq, k0, lk, t0;
+    int valid;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two fp32 fused multiply-adds / additions in one instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, float a0, float a1, float b, float c) {
+    asm("{\n.reg .b64 p, q, r;\nmov.b64 p, {%2, %3};\nmov.b64 q, {%4, %4};\nmov.b64 r, {%5, %5};\n"
+        "fma.rn.f32x2 p, p, q, r;\nmov.b64 {%0, %1}, p;\n}"
+        : "=f"(x), "=f"(y)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a0, float a1) {
+    asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nadd.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}"
+        : "+f"(x), "+f"(y)
+        : "f"(a0), "f"(a1));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if (std::is_same<T, __half>::value) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// The registers of earlier tensor-memory loads may be used from here on.
+template <int N> __device__ __forceinline__ void loaded(float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Operand whose rows run along the MMA's K and whose contiguous side is M or N (V): 64-element
+// blocks lbo bytes apart, groups of 8 rows 1024 bytes apart, 128-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t lbo_bytes) {
+    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t((lbo_bytes >> 4) & 0x3FFFu) << 16) |
+           (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// Clamped [cu[s], cu[s + 1]) as (first, length).
+__device__ __forceinline__ void seq_bounds(const int32_t *cu, int64_t s, int64_t most, int &first, int &len) {
+    const int64_t a = min(max(int64_t(cu[s]), int64_t(0)), most), b = min(max(int64_t(cu[s + 1]), int64_t(0)), most);
+    first = int(a);
+    len = int(max(b - a, int64_t(0)));
+}
+
+// The tile'th tile of `span` tokens, counted over the sequences in order.  One warp.
+__device__ __forceinline__ void find_item(const TcArgs &a, int64_t tile, int span, int lane, Item &it) {
+    it.valid = 0;
+    if (!a.cu_q) {
+        it = {0, int(a.tokens_q), 0, int(a.tokens_k), int(tile * span), tile * span < a.tokens_q};
+        return;
+    }
+    int64_t before = 0;
+    for (int64_t s0 = 0; s0 < a.n_seqs; s0 += 32) {
+        const int64_t s = s0 + lane;
+        int q0 = 0, lq = 0;
+        if (s < a.n_seqs) seq_bounds(a.cu_q, s, a.tokens_q, q0, lq);
+        const int64_t tiles = (int64_t(lq) + span - 1) / span;
+        int64_t incl = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const int64_t first = before + incl - tiles;
+        const unsigned hit = __ballot_sync(0xffffffffu, tile >= first && tile < first + tiles);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            const int64_t ss = s0 + src;
+            it.q0 = __shfl_sync(0xffffffffu, q0, src);
+            it.lq = __shfl_sync(0xffffffffu, lq, src);
+            it.t0 = int((tile - __shfl_sync(0xffffffffu, first, src)) * span);
+            seq_bounds(a.cu_k, ss, a.tokens_k, it.k0, it.lk);
+            it.valid = 1;
+            return;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+// Keys that query token t of the sequence sees.
+__device__ __forceinline__ int visible(const TcArgs &a, const Item &it, int t) {
+    if (!a.causal) return it.lk;
+    const int64_t n = int64_t(t) + 1 + it.lk - it.lq;
+    return int(min(max(n, int64_t(0)), int64_t(it.lk)));
+}
+
+template <typename T> struct Bits;
+template <> struct Bits<__half> {
+    static constexpr uint32_t kExp = 0x7c007c00u, kOne = 0x04000400u;
+};
+template <> struct Bits<__nv_bfloat16> {
+    static constexpr uint32_t kExp = 0x7f807f80u, kOne = 0x00800080u;
+};
+// Nonzero (bits 15 and 31) where one of the two packed values is infinite or NaN.
+template <typename T> __device__ __forceinline__ uint32_t nonfinite2(uint32_t u) {
+    return ((u & Bits<T>::kExp) + Bits<T>::kOne) & 0x80008000u;
+}
+
+// A tile's V rows [from, end) may be unseen by some rows, and the rows from `end` on belong to
+// nobody: a weight of zero times what they hold must stay zero.  Rows from `end` on become
+// zeros; an infinity or NaN before `end` becomes zero and is reported (the rows that see it
+// take it in at the end).  One warp, on a tile of DP/64 blocks of 128 x 128 bytes.
+template <typename T, int DP> __device__ __forceinline__ bool clean_values(uint8_t *tile, int from, int end, int lane) {
+    uint32_t seen = 0;
+    for (int b = 0; b < DP / 64; ++b) {
+        uint4 *rows = reinterpret_cast<uint4 *>(tile + b * kKeys * 128);
+        for (int i = from * 8 + lane; i < end * 8; i += 32) {
+            const uint4 u = rows[i];
+            const uint32_t x = nonfinite2<T>(u.x), y = nonfinite2<T>(u.y), z = nonfinite2<T>(u.z), w = nonfinite2<T>(u.w);
+            if (x | y | z | w) {
+                auto keep = [](uint32_t v, uint32_t bad) {
+                    if (bad & 0x8000u) v &= 0xffff0000u;
+                    if (bad & 0x80000000u) v &= 0x0000ffffu;
+                    return v;
+                };
+                rows[i] = make_uint4(keep(u.x, x), keep(u.y, y), keep(u.z, z), keep(u.w, w));
+                seen = 1;
+            }
+        }
+        for (int i = end * 8 + lane; i < kKeys * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+    return __any_sync(0xffffffffu, seen != 0);
+}
+
+struct Bars {
+    uint64_t q, full[8], empty[8], clean[8], s[2], p[2], o[2], drain;
+};
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ TcArgs a) {
+    using P = Plan<DP>;
+    constexpr int ST = P::kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ Bars bars;
+    __shared__ Item item_s;
+    __shared__ uint32_t tmem_s;
+    __shared__ int abort_s, odd_values;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (blockIdx.x == 0 && tid == 0) *a.status = QMM_OK;
+
+    // blocks in order: all heads and splits of a tile, the last tiles (most keys) first
+    int64_t rest = int64_t(gridDim.x) - 1 - blockIdx.x;
+    const int hk = int(rest % a.shape.hk);
+    rest /= a.shape.hk;
+    const int split = int(rest % a.splits);
+    const int64_t tile = rest / a.splits;
+
+    if (warp == 9) {
+        Item it;
+        find_item(a, tile, 2 * a.per_half, lane, it);
+        if (lane == 0) {
+            item_s = it;
+            abort_s = 0;
+            odd_values = 0;
+            mbar_init(smem_u32(&bars.q), 1);
+            for (int i = 0; i < ST; ++i) {
+                mbar_init(smem_u32(&bars.full[i]), 1);
+                mbar_init(smem_u32(&bars.empty[i]), 1);
+                mbar_init(smem_u32(&bars.clean[i]), 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&bars.s[i]), 1);
+                mbar_init(smem_u32(&bars.p[i]), 4);
+                mbar_init(smem_u32(&bars.o[i]), 1);
+            }
+            mbar_init(smem_u32(&bars.drain), 1);
+            fence_mbar_init();
+        }
+    }
+    __syncthreads();
+    const Item it = item_s;
+    if (!it.valid) return;
+    if (warp == 8) {
+        tmem_alloc(smem_u32(&tmem_s), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_s;
+    volatile int *abort = &abort_s;
+
+    const uint32_t sm0 = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t sq = sm0, skv = sm0 + 2 * P::kTile;
+
+    // key tiles [ja, jb[i]) of each half; vis_lo: the keys that every row of the CTA sees
+    const int half_tokens = a.per_half;
+    const int vis_lo = visible(a, it, it.t0);
+    int n[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int first = it.t0 + i * half_tokens, last = min(first + half_tokens, it.lq) - 1;
+        n[i] = last >= first ? (visible(a, it, last) + kKeys - 1) / kKeys : 0;
+    }
+    const int n_all = max(n[0], n[1]), per_split = (n_all + a.splits - 1) / a.splits;
+    const int ja = min(split * per_split, n_all), je = min(ja + per_split, n_all);
+    const int jb0 = max(min(je, n[0]), ja), jb1 = max(min(je, n[1]), ja);
+    const int jb = max(jb0, jb1);
+
+    if (warp >= 8) {
+    regs_dec<kOtherRegs>();
+    if (warp == 8) {
+        // ------------------------------------------------ copies
+        const int t_row = it.q0 + it.t0;
+        bool ok = true;
+        int issued = 0;
+        // After tile j's copy has arrived.  The tiles to clean lie within the 255 keys that the
+        // CTA's first and last row differ by, at most 3, so no stage is cleaned twice.
+        auto clean = [&](int j) {
+            if ((j + 1) * kKeys <= vis_lo) return;
+            const int item = 2 * (j - ja) + 1, stg = item % ST;
+            ok = mbar_wait(smem_u32(&bars.full[stg]), (item / ST) & 1, abort);
+            if (!ok) return;
+            const bool odd = clean_values<T, DP>(raw + (sm0 - smem_u32(raw)) + (2 + stg) * P::kTile,
+                                                 max(vis_lo - j * kKeys, 0), min(it.lk - j * kKeys, kKeys), lane);
+            if (lane == 0) {
+                if (odd) odd_values = 1;
+                mbar_arrive(smem_u32(&bars.clean[stg]));
+            }
+            __syncwarp();
+        };
+        if (jb > ja && lane == 0) {
+            prefetch_tmap(&a.q);
+            prefetch_tmap(&a.k);
+            prefetch_tmap(&a.v);
+            const uint32_t bar = smem_u32(&bars.q), box = uint32_t(a.group * half_tokens) * 128;
+            const bool both = jb1 > ja, one = jb0 > ja;
+            mbar_arrive_expect_tx(bar, box * (DP / 64) * (uint32_t(one) + uint32_t(both)));
+            for (int i = 0; i < 2; ++i)
+                for (int b = 0; b < DP / 64; ++b)
+                    if (i ? both : one)
+                        tma_load_3d(sq + i * P::kTile + b * kRows * 128, &a.q, b * 64, hk * a.group,
+                                    t_row + i * half_tokens, bar);
+        }
+        for (int j = ja; j < jb && ok; ++j) {
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+                const int item = 2 * (j - ja) + kv, stg = item % ST;
+                if (item >= ST) ok = mbar_wait(smem_u32(&bars.empty[stg]), ((item / ST) - 1) & 1, abort);
+                if (ok && lane == 0) {
+                    const uint32_t bar = smem_u32(&bars.full[stg]);
+                    mbar_arrive_expect_tx(bar, P::kTile);
+                    for (int b = 0; b < DP / 64; ++b)
+                        tma_load_3d(skv + stg * P::kTile + b * kKeys * 128, kv ? &a.v : &a.k, b * 64, hk,
+                                    it.k0 + j * kKeys, bar);
+                }
+                if (ok) issued = item + 1;
+                __syncwarp();
+            }
+            // a tile is cleaned once the next one's copies are under way
+            if (ok && j > ja) clean(j - 1);
+        }
+        if (ok && jb > ja) clean(jb - 1);
+        if (!ok) {  // a wait gave up: the copies in flight land before shared memory is released
+            int never = 0;
+            mbar_wait(smem_u32(&bars.q), 0, &never);
+            for (int item = max(issued - ST, 0); item < issued; ++item) {
+                never = 0;
+                mbar_wait(smem_u32(&bars.full[item % ST]), (item / ST) & 1, &never);
+            }
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------ products
+        if (lane == 0 && jb > ja) {
+            bool ok = mbar_wait_spin(smem_u32(&bars.q), 0, abort);
+            auto full = [&](int item) {
+                ok = ok && mbar_wait_spin(smem_u32(&bars.full[item % ST]), (item / ST) & 1, abort);
+            };
+            auto qk = [&](int i, int j) {
+                const uint32_t kt = skv + uint32_t((2 * (j - ja)) % ST) * P::kTile, qt = sq + i * P::kTile;
+#pragma unroll
+                for (int s = 0; s < DP / 16; ++s) {
+                    const uint32_t off = uint32_t(s / 4) * kRows * 128 + uint32_t(s % 4) * 32;
+                    mma_f16(tmem + i * kKeys, smem_desc(qt + off, 1024, 2), smem_desc(kt + off, 1024, 2), a.idesc_qk,
+                            s != 0);
+                }
+                mma_commit(smem_u32(&bars.s[i]));
+            };
+            full(0);
+            tc_fence_after();
+            if (ok && jb0 > ja) qk(0, ja);
+            if (ok && jb1 > ja) qk(1, ja);
+            if (ok) mma_commit(smem_u32(&bars.empty[0]));
+            for (int j = ja; j < jb && ok; ++j) {
+                const int vi = 2 * (j - ja) + 1, ki = vi + 1;
+                const uint32_t vt = skv + uint32_t(vi % ST) * P::kTile;
+                full(vi);
+                if (ok && (j + 1) * kKeys > vis_lo) ok = mbar_wait_spin(smem_u32(&bars.clean[vi % ST]), 0, abort);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int end = i ? jb1 : jb0;
+                    if (j >= end || !ok) continue;
+                    ok = mbar_wait_spin(smem_u32(&bars.p[i]), (j - ja) & 1, abort);
+                    if (!ok) continue;
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = 0; s < kKeys / 16; ++s)
+                        mma_f16_tmem_a(tmem + 256 + i * DP, tmem + i * kKeys + s * 8,
+                                       smem_desc_mn(vt + s * 16 * 128, kKeys * 128), a.idesc_pv, j > ja || s > 0);
+                    if (j + 1 < end) {
+                        full(ki);
+                        if (ok) qk(i, j + 1);
+                    } else {
+                        mma_commit(smem_u32(&bars.o[i]));
+                    }
+                }
+                if (ok) mma_commit(smem_u32(&bars.empty[vi % ST]));
+                if (ok && j + 1 < jb) mma_commit(smem_u32(&bars.empty[ki % ST]));
+            }
+            if (!ok) {  // let what was issued end before the tensor memory is freed
+                mma_commit(smem_u32(&bars.drain));
+                int never = 0;
+                mbar_wait_spin(smem_u32(&bars.drain), 0, &never);
+            }
+        }
+    }
+    } else {
+        // ------------------------------------------------ softmax, one row a thread
+        regs_inc<kSoftmaxRegs>();
+        const int i = warp >> 2, r = tid & 127, end = i ? jb1 : jb0;
+        const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 256 + i * DP;
+        const int t = it.t0 + i * half_tokens + r / a.group;
+        const bool row_valid = r < half_tokens * a.group && t < it.lq;
+        const int vis = row_valid ? visible(a, it, t) : 0;
+        // the keys that every row of this half sees
+        const int vis_half = visible(a, it, it.t0 + i * half_tokens);
+        float top = -INFINITY, sum0 = 0.f, sum1 = 0.f;
+        bool ok = true;
+        for (int j = ja; j < end; ++j) {
+            ok = mbar_wait(smem_u32(&bars.s[i]), (j - ja) & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            float s[kKeys];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + c * 32, *reinterpret_cast<float(*)[32]>(s + c * 32));
+            tmem_ld_wait();
+            loaded(s);
+            if ((j + 1) * kKeys > vis_half) {
+                const int left = vis - j * kKeys;
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c)
+                    if (c >= left) s[c] = -INFINITY;
+            }
+            float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+            for (int c = 4; c < kKeys; c += 8) {
+                m0 = max3(m0, s[c], s[c + 1]);
+                m1 = max3(m1, s[c + 2], s[c + 3]);
+                if (c + 4 < kKeys) {
+                    m2 = max3(m2, s[c + 4], s[c + 5]);
+                    m3 = max3(m3, s[c + 6], s[c + 7]);
+                }
+            }
+            const float most = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+            // move the maximum when a score passes it by more than the slack
+            const bool move = (most - top) * a.scale_log2 > kSlack || (top == -INFINITY && most > -INFINITY);
+            if (j == ja) {
+                if (move) top = most;
+            } else if (__any_sync(0xffffffffu, move)) {
+                const float base = move ? most : top;
+                const float f = top == -INFINITY ? 1.f : ex2((top - base) * a.scale_log2);
+                top = base;
+                sum0 *= f;
+                sum1 *= f;
+                // S_i(j) was issued after O_i's last product, so that one is done
+#pragma unroll
+                for (int c = 0; c < DP / 32; ++c) {
+                    float o[32];
+                    tmem_ld_32x32b_x32(o_addr + c * 32, o);
+                    tmem_ld_wait();
+                    loaded(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= f;
+                    tmem_st_32x32b_x32(o_addr + c * 32, o);
+                }
+            }
+            const float shift = top == -INFINITY ? 0.f : -top * a.scale_log2;
+#pragma unroll
+            for (int c = 0; c < kKeys / 32; ++c) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int x = c * 32 + 2 * e;
+                    fma2(s[x], s[x + 1], s[x], s[x + 1], a.scale_log2, shift);
+                    s[x] = ex2(s[x]);
+                    s[x + 1] = ex2(s[x + 1]);
+                    p[e] = pack2<T>(s[x], s[x + 1]);
+                }
+                tmem_st_32x32b_x16(s_addr + c * 16, p);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.p[i]));
+            // the row's sum, of the unrounded weights, while the product runs
+            float a0 = s[0], a1 = s[1], b0 = s[2], b1 = s[3];
+#pragma unroll
+            for (int c = 4; c < kKeys; c += 4) {
+                add2(a0, a1, s[c], s[c + 1]);
+                add2(b0, b1, s[c + 2], s[c + 3]);
+            }
+            add2(a0, a1, b0, b1);
+            add2(sum0, sum1, a0, a1);
+        }
+        if (ok && end > ja) ok = mbar_wait(smem_u32(&bars.o[i]), 0, abort);
+        if (ok) {
+            tc_fence_after();
+            const float sum = end > ja ? sum0 + sum1 : 0.f;
+            const bool none = !(sum != 0.f);  // no key seen (a NaN sum is not none)
+            const float inv = none ? 0.f : 1.f / sum;
+            const int head = hk * a.group + r % a.group;
+            const int64_t row = (int64_t(it.q0) + t) * a.shape.hq + head;
+            const bool odd = end > ja && *(volatile int *)&odd_values;
+            const int odd_from = max(vis_lo, ja * kKeys), odd_to = min(vis, end * kKeys);
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {
+                float o[32];
+                if (end > ja) {
+                    tmem_ld_32x32b_x32(o_addr + c * 32, o);
+                    tmem_ld_wait();
+                    loaded(o);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                if (!row_valid || c * 32 >= a.shape.d) continue;
+                if (odd) {
+                    const T *v = static_cast<const T *>(a.v_data) + hk * a.sv.h + c * 32;
+                    for (int key = odd_from; key < odd_to; ++key) {
+                        const T *vr = v + (int64_t(it.k0) + key) * a.sv.t;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (c * 32 + e >= a.shape.d) continue;
+                            const float x = float(vr[e]);
+                            if (!isfinite(x)) o[e] += x;
+                        }
+                    }
+                }
+                if (a.splits == 1) {
+                    T *dst = static_cast<T *>(a.out) + (int64_t(it.q0) + t) * a.so.t + head * a.so.h + c * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        if (c * 32 + e < a.shape.d)
+                            *reinterpret_cast<uint4 *>(dst + e) =
+                                make_uint4(pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
+                                           pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
+                } else {
+                    float *dst = a.part + (int64_t(split) * a.tokens_q * a.shape.hq + row) * a.shape.d + c * 32;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        if (c * 32 + e < a.shape.d)
+                            *reinterpret_cast<float4 *>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+            if (row_valid) {
+                const float l2 = none ? -INFINITY : top * a.scale_log2 + log2f(sum);
+                if (a.splits > 1) a.part_lse[int64_t(split) * a.tokens_q * a.shape.hq + row] = l2;
+                else if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (*abort && tid == 0) *a.status = QMM_ERR_DEVICE;
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// out[row] = sum_s 2^(lse_s - top) part_s[row] / sum_s 2^(lse_s - top); one warp a row.
+template <typename T>
+__global__ void __launch_bounds__(128) attn_join_kernel(const float *part, const float *part_lse, int parts,
+                                                        int64_t rows, HeadShape shape, T *out, HeadStrides so,
+                                                        float *lse) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    float top = -INFINITY;
+    for (int s = lane; s < parts; s += 32) top = fmaxf(top, part_lse[s * rows + row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool live = 4 * lane < shape.d;
+    for (int s = 0; s < parts; ++s) {
+        const float l = part_lse[s * rows + row];
+        if (l == -INFINITY) continue;
+        const float w = ex2(l - base);
+        sum += w;
+        if (live) {
+            const float4 p = *reinterpret_cast<const float4 *>(part + (s * rows + row) * shape.d + 4 * lane);
+            acc.x += w * p.x;
+            acc.y += w * p.y;
+            acc.z += w * p.z;
+            acc.w += w * p.w;
+        }
+    }
+    const bool none = !(sum != 0.f);
+    const float inv = none ? 0.f : 1.f / sum;
+    const int64_t t = row / shape.hq;
+    const int h = int(row % shape.hq);
+    if (live)
+        *reinterpret_cast<uint2 *>(out + t * so.t + h * so.h + 4 * lane) =
+            make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+    if (lse && lane == 0) lse[row] = none ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
+}
+
+// A [tokens][heads][d] view as a 3-dimensional map with boxes of 64 elements x heads x tokens.
+bool make_map(CUtensorMap *map, qmm_float t, const void *data, int d, int64_t heads, int64_t tokens, HeadStrides s,
+              int box_heads, int box_tokens) {
+    const uint64_t dims[3] = {uint64_t(d), uint64_t(heads), uint64_t(tokens)};
+    // a stride that is never taken still has to be a valid one
+    const uint64_t strides[2] = {uint64_t(heads > 1 ? s.h : d) * 2, uint64_t(tokens > 1 ? s.t : d) * 2};
+    const uint32_t box[3] = {64, uint32_t(box_heads), uint32_t(box_tokens)};
+    return tc_make_map(map, t == QMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, data,
+                       dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <typename T, int DP> cudaError_t launch_dp(const TcArgs &a, int64_t blocks, cudaStream_t st) {
+    auto kern = attn_tc_kernel<T, DP>;
+    cudaError_t e = ensure_smem(kern, Plan<DP>::kBytes);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)blocks, kTcThreads, Plan<DP>::kBytes, st>>>(a);
+    return cudaGetLastError();
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int64_t prompt_tiles(const PromptArgs &a) {
+    const int64_t span = 2 * (kRows / (a.shape.hq / a.shape.hk));
+    // each sequence ends in at most one partial tile, and holds at least one token per tile
+    return std::min(a.tokens_q, a.tokens_q / span + (a.cu_q || a.n_seqs > 1 ? a.n_seqs : 1));
+}
+
+}  // namespace
+
+// Key splits of a prompt call: one, unless the tiles leave most SMs idle and the keys are many.
+int attn_prompt_splits(const PromptArgs &) { return 1; }
+
+size_t attn_prompt_workspace_bytes(const PromptArgs &a) {
+    const int splits = attn_prompt_splits(a);
+    if (splits == 1) return 256;
+    const size_t rows = size_t(a.tokens_q) * a.shape.hq;
+    return 256 + align256(size_t(splits) * rows * a.shape.d * 4) + align256(size_t(splits) * rows * 4);
+}
+
+cudaError_t launch_attn_prompt(const PromptArgs &p, qmm_float t, void *ws, cudaStream_t st) {
+    TcArgs a{};
+    const int g = p.shape.hq / p.shape.hk, per_half = kRows / g;
+    if (!make_map(&a.q, t, p.q, p.shape.d, p.shape.hq, p.tokens_q, p.sq, g, per_half)) return cudaErrorInvalidValue;
+    // without any key the maps are not used; they describe q then
+    const bool keys = p.tokens_k > 0;
+    if (!make_map(&a.k, t, keys ? p.k : p.q, p.shape.d, keys ? p.shape.hk : 1, keys ? p.tokens_k : 1, p.sk, 1, kKeys) ||
+        !make_map(&a.v, t, keys ? p.v : p.q, p.shape.d, keys ? p.shape.hk : 1, keys ? p.tokens_k : 1, p.sv, 1, kKeys))
+        return cudaErrorInvalidValue;
+    a.out = p.out;
+    a.lse = p.lse;
+    a.v_data = p.v;
+    a.so = p.so;
+    a.sv = p.sv;
+    a.shape = p.shape;
+    a.cu_q = p.cu_q;
+    a.cu_k = p.cu_k;
+    a.n_seqs = p.n_seqs;
+    a.tokens_q = p.tokens_q;
+    a.tokens_k = p.tokens_k;
+    a.group = g;
+    a.per_half = per_half;
+    a.causal = p.causal;
+    a.splits = attn_prompt_splits(p);
+    // a scale of 0 (all keys alike) as the smallest one, so that a hidden key's -infinity stays one;
+    // a negative scale negates Q in the product
+    a.scale_log2 = std::max(std::abs(p.scale) * kLog2e, 1.2e-38f);
+    const int dp = p.shape.d <= 64 ? 64 : 128;
+    const uint32_t type_bits = t == QMM_F16 ? 0u : (1u << 7) | (1u << 10);
+    a.idesc_qk = idesc_f16_f32(kRows, kKeys) | type_bits | (p.scale < 0.f ? 1u << 13 : 0u);
+    a.idesc_pv = idesc_f16_f32(kRows, dp) | type_bits | (1u << 16);
+    a.status = static_cast<int *>(ws);
+    const int64_t rows = p.tokens_q * p.shape.hq;
+    if (a.splits > 1) {
+        a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
+        a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256 +
+                                               align256(size_t(a.splits) * rows * p.shape.d * 4));
+    }
+    const int64_t blocks = prompt_tiles(p) * a.splits * p.shape.hk;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    cudaError_t e;
+    if (t == QMM_F16) e = dp == 64 ? launch_dp<__half, 64>(a, blocks, st) : launch_dp<__half, 128>(a, blocks, st);
+    else e = dp == 64 ? launch_dp<__nv_bfloat16, 64>(a, blocks, st) : launch_dp<__nv_bfloat16, 128>(a, blocks, st);
+    if (e != cudaSuccess || a.splits == 1) return e;
+    const unsigned grid = (unsigned)((rows + 3) / 4);
+    if (t == QMM_F16)
+        attn_join_kernel<__half><<<grid, 128, 0, st>>>(a.part, a.part_lse, a.splits, rows, p.shape,
+                                                       static_cast<__half *>(p.out), p.so, p.lse);
+    else
+        attn_join_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a.part, a.part_lse, a.splits, rows, p.shape,
+                                                              static_cast<__nv_bfloat16 *>(p.out), p.so, p.lse);
+    return cudaGetLastError();
+}
+
+}  // namespace qmm

@@ -72,8 +72,13 @@ __device__ __forceinline__ uint4 nibbles5_to_f16(uint32_t w0, uint32_t w1, uint3
     return r;
 }
 
+// A tiled tensor map of `rank` dimensions (innermost first; strides in bytes from the second
+// dimension on).  The driver's encoder is looked up once.  False on any failure.
+bool tc_make_map(CUtensorMap *map, CUtensorMapDataType dt, int rank, const void *base, const uint64_t *dims,
+                 const uint64_t *strides, const uint32_t *box, CUtensorMapSwizzle sw);
+
 // A 2D tiled tensor map over a row-major [outer][inner] array with the given row
-// stride (host; the driver's encoder is looked up once).  False on any failure.
+// stride.  False on any failure.
 bool tc_make_map_2d(CUtensorMap *map, CUtensorMapDataType dt, int esize, const void *base, uint64_t inner,
                     uint64_t outer, uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer,
                     CUtensorMapSwizzle sw);
