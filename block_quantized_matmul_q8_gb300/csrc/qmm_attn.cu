@@ -1,136 +1,477 @@
-// qmm_attn.cu -- attention of a decoding batch.
+// qmm_attn.cu -- attention of a decoding batch: one query token a request, over its own cache
+// and, in the same pass or joined from the tensor-core phase, the prefix that all requests share.
 //
-//   out = sum_j p_j v_j,  p = softmax_j(scale q.k_j) over the keys that the row sees.
+//   out = sum_j p_j v_j,  p = softmax_j(scale q.k_j) over the prefix rows and the cache rows.
 //
-// One warp takes one (query token, query head) row and streams its keys in one pass with a
-// running maximum and sum (fp32): lane l holds the elements 4l..4l+3 of q, of each key and of
-// the output.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+// Bound by reading the keys and values once.  A cluster of up to 16 CTAs takes one request and
+// kv head (up to 16 query heads of it, the rows of one warp-level MMA): its key tiles of 64 are
+// shared out among the CTAs, each streams them through a ring of TMA copies, and each of its 4
+// warps keeps the running softmax of its own 16 keys of every tile, so no warp waits for another.
+// The partial rows stay in shared memory and are joined through the cluster: no second launch
+// and no workspace.  The products run on mma.sync: with 16 rows the copies take an order of
+// magnitude longer than the tensor work, and tcgen05's 128 rows would stay empty.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
-#include "qmm_attn.h"
+#include "qmm_attn.cuh"
 #include "qmm_internal.h"
+#include "qmm_tc_ptx.cuh"
 
 namespace qmm {
 
 namespace {
 
-constexpr int kRowWarps = 4;
-constexpr int kBatch = 4;  // keys of one step
+using namespace ptx;
 
-__device__ __forceinline__ float4 load4(const __half *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&u.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-}
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                       __uint_as_float(u.y & 0xffff0000u));
-}
-__device__ __forceinline__ void store4(__half *p, float4 v) {
-    p[0] = __float2half_rn(v.x);
-    p[1] = __float2half_rn(v.y);
-    p[2] = __float2half_rn(v.z);
-    p[3] = __float2half_rn(v.w);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
-    p[0] = __float2bfloat16_rn(v.x);
-    p[1] = __float2bfloat16_rn(v.y);
-    p[2] = __float2bfloat16_rn(v.z);
-    p[3] = __float2bfloat16_rn(v.w);
-}
+constexpr int kTileKeys = 64;
+constexpr int kWarps = 4;              // each takes 16 keys of a tile
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kMaxRows = 16;           // query heads of one CTA
+constexpr int kMaxCluster = 16;
 
-// The running softmax of one row: maximum of scale*q.k so far, sum of exp(score - top), and
-// the weighted sum of the values (this lane's four elements).
-struct Row {
-    float top = -INFINITY, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+template <int DP> struct Ring {
+    static constexpr int kHalf = kTileKeys * DP * 2;  // a K or a V tile: DP/64 blocks of 64 x 128 bytes
+    static constexpr int kStages = DP == 128 ? 3 : 6;
+    static constexpr int kPartStride = DP + 4;        // floats between a warp's partial rows
+    static constexpr size_t kBytes = size_t(2 * kStages) * kHalf + 1024;
+    static constexpr int kParts = kWarps * kMaxRows * kPartStride;  // floats of the CTA's partial rows
+    static_assert((kParts + kMaxRows * (kMaxCluster * kWarps + kMaxPrefixParts + 2)) * 4 <= 2 * kStages * kHalf,
+                  "partial rows and weights reuse the ring");
 };
 
-template <typename T>
-__device__ __forceinline__ void take_keys(Row &s, float4 q, const T *k, const T *v, int64_t k_stride,
-                                          int64_t v_stride, int64_t n, bool live) {
-    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t j = 0; j < n; j += kBatch) {
-        float z[kBatch];
-        float4 vv[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const bool on = live && j + i < n;
-            const float4 kk = on ? load4(k + (j + i) * k_stride) : zero;
-            vv[i] = on ? load4(v + (j + i) * v_stride) : zero;
-            z[i] = q.x * kk.x + q.y * kk.y + q.z * kk.z + q.w * kk.w;
+struct DecArgs {
+    CUtensorMap k, v, pk, pv;
+    DecodeArgs d;
+    int group, row_blocks;   // query heads of a kv head, blocks of 16 of them
+    int64_t inline_prefix;   // prefix rows that this launch reads itself
+    int parts;               // partial rows of the tensor-core phase to join
+    const float *part, *part_lse;
+    float scale_log2;
+    int *status;
+};
+
+template <typename T> __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (std::is_same<T, __half>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// A float of another CTA's shared memory, at this CTA's address `addr`.
+__device__ __forceinline__ float peer_f32(uint32_t addr, uint32_t rank) {
+    uint32_t p;
+    float v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 peer_f32x4(uint32_t addr, uint32_t rank) {
+    uint32_t p;
+    float4 v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(p)
+                 : "memory");
+    return v;
+}
+
+// Byte of 16-byte unit u of a row in a block of rows of 128 bytes, 128-byte swizzled.
+__device__ __forceinline__ uint32_t swizzled(int row, int u) { return uint32_t(row * 128 + ((u ^ (row & 7)) << 4)); }
+
+template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_constant__ DecArgs a) {
+    using R = Ring<DP>;
+    constexpr int ST = R::kStages, KS = DP / 16;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[ST], empty[ST];
+    __shared__ int abort_s;
+    __shared__ float ml_s[kWarps][kMaxRows][2];  // each warp's maximum and sum (log2 domain)
+    const DecodeArgs &d = a.d;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
+    int64_t rest = blockIdx.x / ranks;
+    const int block = int(rest % a.row_blocks);
+    rest /= a.row_blocks;
+    const int hk = int(rest % d.shape.hk);
+    const int64_t b = rest / d.shape.hk;
+    const int head0 = hk * a.group + block * kMaxRows, rows = min(a.group - block * kMaxRows, kMaxRows);
+    if (blockIdx.x == 0 && tid == 0 && a.parts == 0) *a.status = QMM_OK;
+
+    const int64_t len = d.room > 0 ? min(max(int64_t(d.lens[b]), int64_t(0)), d.room) : 0;
+    const int64_t ptiles = (a.inline_prefix + kTileKeys - 1) / kTileKeys;
+    const int64_t tiles = ptiles + (len + kTileKeys - 1) / kTileKeys, per = (tiles + ranks - 1) / ranks;
+    const int64_t j0 = min(rank * per, tiles), j1 = min(j0 + per, tiles);
+    const int n = int(j1 - j0);
+
+    const uint32_t sm = (smem_u32(raw) + 1023u) & ~1023u;
+    if (tid == 0) {
+        abort_s = 0;
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), kWarps);
         }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            for (int o = 16; o > 0; o >>= 1) z[i] += __shfl_xor_sync(0xffffffffu, z[i], o);
-            if (j + i >= n) z[i] = -INFINITY;
-        }
-        float top = s.top;
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) top = fmaxf(top, z[i]);
-        const float base = top == -INFINITY ? 0.f : top;
-        const float f = expf(s.top - base);
-        s.sum *= f;
-        s.acc = make_float4(s.acc.x * f, s.acc.y * f, s.acc.z * f, s.acc.w * f);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (j + i >= n) continue;
-            const float p = expf(z[i] - base);
-            s.sum += p;
-            s.acc.x += p * vv[i].x;
-            s.acc.y += p * vv[i].y;
-            s.acc.z += p * vv[i].z;
-            s.acc.w += p * vv[i].w;
-        }
-        s.top = top;
+        fence_mbar_init();
     }
+    __syncthreads();
+    volatile int *abort = &abort_s;
+
+    if (warp == kWarps) {
+        // ------------------------------------------------ copies
+        bool ok = true;
+        int issued = 0;
+        if (lane == 0) {
+            for (int i = 0; i < n && ok; ++i) {
+                const int stg = i % ST;
+                if (i >= ST) ok = mbar_wait(smem_u32(&empty[stg]), ((i / ST) - 1) & 1, abort);
+                if (!ok) break;
+                const uint32_t bar = smem_u32(&full[stg]), dst = sm + stg * 2 * R::kHalf;
+                mbar_arrive_expect_tx(bar, 2 * R::kHalf);
+                const int64_t j = j0 + i;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+                    for (int c = 0; c < DP / 64; ++c) {
+                        const uint32_t to = dst + kv * R::kHalf + c * kTileKeys * 128;
+                        if (j < ptiles) tma_load_3d(to, kv ? &a.pv : &a.pk, c * 64, hk, int(j * kTileKeys), bar);
+                        else tma_load_4d(to, kv ? &a.v : &a.k, c * 64, hk, int((j - ptiles) * kTileKeys), int(b), bar);
+                    }
+                issued = i + 1;
+            }
+            if (!ok)  // a wait gave up: the copies in flight land before the ring is reused or released
+                for (int i = max(issued - ST, 0); i < issued; ++i) {
+                    int never = 0;
+                    mbar_wait(smem_u32(&full[i % ST]), (i / ST) & 1, &never);
+                }
+        }
+        __syncwarp();
+    }
+
+    // this warp's running softmax of rows lane/4 and lane/4 + 8
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, o[DP / 8][4];
+#pragma unroll
+    for (int c = 0; c < DP / 8; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+    if (warp < kWarps && n > 0) {
+        uint32_t q[KS][4];
+        {
+            const T *src = static_cast<const T *>(d.q) + b * d.sq.t + head0 * d.sq.h;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = (lane >> 2) + (e & 1) * 8, col = ks * 16 + (lane & 3) * 2 + (e >> 1) * 8;
+                    q[ks][e] = row < rows && col < d.shape.d
+                                   ? *reinterpret_cast<const uint32_t *>(src + row * d.sq.h + col)
+                                   : 0u;
+                }
+        }
+        for (int i = 0; i < n; ++i) {
+            const int stg = i % ST;
+            if (!mbar_wait(smem_u32(&full[stg]), (i / ST) & 1, abort)) break;
+            const int64_t j = j0 + i;
+            const int64_t left = j < ptiles ? a.inline_prefix - j * kTileKeys : len - (j - ptiles) * kTileKeys;
+            const int valid = int(min(left, int64_t(kTileKeys))) - warp * 16;  // of this warp's keys
+            if (valid > 0) {
+                const uint32_t kt = sm + stg * 2 * R::kHalf, vt = kt + R::kHalf;
+                if (valid < 16) {
+                    // rows that nobody owns may hold anything: zero weights times them must be zero
+                    uint8_t *v = raw + (vt - smem_u32(raw));
+                    for (int c = 0; c < DP / 64; ++c)
+                        for (int u = valid * 8 + lane; u < 16 * 8; u += 32)
+                            reinterpret_cast<uint4 *>(v + c * kTileKeys * 128 + warp * 16 * 128)[u] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                float s[2][4] = {};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t f[4];  // keys 0-7 and 8-15, each k 0-7 and 8-15
+                    const int key = warp * 16 + (lane & 7) + ((lane >> 4) << 3), u = (ks & 3) * 2 + ((lane >> 3) & 1);
+                    ldsm4(f, kt + (ks >> 2) * kTileKeys * 128 + swizzled(key, u));
+                    mma16816<T>(s[0], q[ks], f[0], f[1]);
+                    mma16816<T>(s[1], q[ks], f[2], f[3]);
+                }
+                float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = t * 8 + (lane & 3) * 2 + (e & 1);
+                        s[t][e] = key < valid ? s[t][e] * a.scale_log2 : -INFINITY;
+                        m[e >> 1] = fmaxf(m[e >> 1], s[t][e]);
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 1));
+                    m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 2));
+                }
+                if (__any_sync(0xffffffffu, m[0] > top[0] || m[1] > top[1])) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float now = fmaxf(top[h], m[h]);
+                        const float f = top[h] == -INFINITY ? 1.f : ex2(top[h] - now);
+                        top[h] = now;
+                        sum[h] *= f;
+#pragma unroll
+                        for (int c = 0; c < DP / 8; ++c) {
+                            o[c][2 * h] *= f;
+                            o[c][2 * h + 1] *= f;
+                        }
+                    }
+                }
+                uint32_t p[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float base = top[h] == -INFINITY ? 0.f : top[h];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const float x = ex2(s[t][2 * h] - base), y = ex2(s[t][2 * h + 1] - base);
+                        sum[h] += x + y;
+                        p[t * 2 + h] = pack2<T>(x, y);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < DP / 16; ++c) {
+                    uint32_t f[4];  // elements 16c..16c+7 of keys 0-7, 8-15, then 16c+8..
+                    const int key = warp * 16 + (lane & 15), u = (c & 3) * 2 + (lane >> 4);
+                    ldsm4_t(f, vt + (c >> 2) * kTileKeys * 128 + swizzled(key, u));
+                    mma16816<T>(o[2 * c], p, f[0], f[1]);
+                    mma16816<T>(o[2 * c + 1], p, f[2], f[3]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&empty[stg]));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+            sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+        }
+    }
+    __syncthreads();  // the ring is free: every copy was waited for
+    float *part = reinterpret_cast<float *>(raw + (sm - smem_u32(raw)));
+    // weights of the partial rows in the join: this request's warps and the tensor-core phase's splits
+    auto weight_s = reinterpret_cast<float(*)[kMaxCluster * kWarps + 1]>(part + R::kParts);
+    auto pweight_s = reinterpret_cast<float(*)[kMaxPrefixParts + 1]>(weight_s + kMaxRows);
+    if (warp < kWarps) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = (lane >> 2) + 8 * h;
+            if (row >= rows) continue;
+            float *dst = part + (warp * kMaxRows + row) * R::kPartStride + (lane & 3) * 2;
+            if (n > 0)
+#pragma unroll
+                for (int c = 0; c < DP / 8; ++c)
+                    *reinterpret_cast<float2 *>(dst + c * 8) = make_float2(o[c][2 * h], o[c][2 * h + 1]);
+            if ((lane & 3) == 0) {
+                ml_s[warp][row][0] = top[h];
+                ml_s[warp][row][1] = sum[h];
+            }
+        }
+    }
+    cluster_sync();
+    if (*abort && tid == 0) *a.status = QMM_ERR_DEVICE;
+
+    // ------------------------------------------------ the join
+    if (a.parts > 0) grid_dependency_wait();
+    const int own = ranks * kWarps;
+    const int64_t row0 = b * d.shape.hq + head0, all_rows = d.batch * d.shape.hq;
+    for (int row = warp; row < rows; row += kWarps + 1) {
+        float most = -INFINITY;
+        for (int p = lane; p < own; p += 32) {
+            const float m = peer_f32(smem_u32(&ml_s[p & (kWarps - 1)][row][0]), p / kWarps);
+            weight_s[row][p] = m;
+            most = fmaxf(most, m);
+        }
+        for (int p = lane; p < a.parts; p += 32) {
+            const float m = a.part_lse[p * all_rows + row0 + row];
+            pweight_s[row][p] = m;
+            most = fmaxf(most, m);
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
+        const float base = most == -INFINITY ? 0.f : most;
+        float total = 0.f;
+        for (int p = lane; p < own; p += 32) {
+            const float l = peer_f32(smem_u32(&ml_s[p & (kWarps - 1)][row][1]), p / kWarps);
+            const float m = weight_s[row][p];
+            const float w = m == -INFINITY && l == 0.f ? 0.f : ex2(m - base);  // 0: no key
+            weight_s[row][p] = w;
+            total += w * l;
+        }
+        for (int p = lane; p < a.parts; p += 32) {
+            const float m = pweight_s[row][p], w = m == -INFINITY ? 0.f : ex2(m - base);
+            pweight_s[row][p] = w;
+            total += w;
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
+        const bool none = !(total != 0.f);
+        const float inv = none ? 0.f : 1.f / total;
+        for (int p = lane; p < own; p += 32) weight_s[row][p] *= inv;
+        for (int p = lane; p < a.parts; p += 32) pweight_s[row][p] *= inv;
+        if (d.lse && lane == 0 && rank == 0) d.lse[row0 + row] = none ? -INFINITY : (base + log2f(total)) * kLn2;
+    }
+    __syncthreads();
+    const int quads = d.shape.d / 4;
+    for (int e = rank * kThreads + tid; e < rows * quads; e += ranks * kThreads) {
+        const int row = e / quads, col = (e - row * quads) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p = 0; p < own; ++p) {
+            const float w = weight_s[row][p];
+            if (w == 0.f) continue;
+            const float4 x = peer_f32x4(
+                smem_u32(part + ((p & (kWarps - 1)) * kMaxRows + row) * R::kPartStride + col), p / kWarps);
+            acc.x += w * x.x;
+            acc.y += w * x.y;
+            acc.z += w * x.z;
+            acc.w += w * x.w;
+        }
+        for (int p = 0; p < a.parts; ++p) {
+            const float w = pweight_s[row][p];
+            if (w == 0.f) continue;
+            const float4 x =
+                *reinterpret_cast<const float4 *>(a.part + (p * all_rows + row0 + row) * d.shape.d + col);
+            acc.x += w * x.x;
+            acc.y += w * x.y;
+            acc.z += w * x.z;
+            acc.w += w * x.w;
+        }
+        T *out = static_cast<T *>(d.out) + b * d.so.t + (head0 + row) * d.so.h + col;
+        *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
+    }
+    cluster_sync();  // no CTA leaves while its shared memory may be read
 }
 
-template <typename T> __device__ __forceinline__ void finish(const Row &s, T *out, float *lse, int lane, bool live) {
-    const float inv = s.sum == 0.f ? 0.f : 1.f / s.sum;
-    if (live) store4(out, make_float4(s.acc.x * inv, s.acc.y * inv, s.acc.z * inv, s.acc.w * inv));
-    if (lse && lane == 0) *lse = s.sum == 0.f ? -INFINITY : s.top + logf(s.sum);
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Whether the prefix goes through the tensor-core phase: the rows of the batch that share a kv
+// head are many enough that reading the prefix once for all of them pays for a second launch.
+bool prefix_on_tensor_cores(const DecodeArgs &d) {
+    return d.prefix > 0 && d.batch * d.prefix > 16384;
 }
 
-__device__ __forceinline__ float4 scaled(float4 q, float f) { return make_float4(q.x * f, q.y * f, q.z * f, q.w * f); }
+// CTAs of one request and kv head: enough for every SM to hold several, two tiles each.
+int cluster_ctas(const DecodeArgs &d, int64_t inline_prefix, int64_t pairs) {
+    const int64_t tiles = (inline_prefix + kTileKeys - 1) / kTileKeys + (d.room + kTileKeys - 1) / kTileKeys;
+    int c = 1;
+    while (c < kMaxCluster && pairs * c < 6 * device_sm_count() && tiles >= 2 * c) c *= 2;
+    return c;
+}
 
-template <typename T> __global__ void __launch_bounds__(kRowWarps * 32) decode_rows_kernel(const DecodeArgs a) {
-    const int lane = threadIdx.x & 31, h = blockIdx.y;
-    const int64_t b = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-    if (b >= a.batch) return;
-    const bool live = 4 * lane < a.shape.d;
-    const int hk = h / (a.shape.hq / a.shape.hk);
-    const float4 q = live ? scaled(load4(static_cast<const T *>(a.q) + b * a.sq.t + h * a.sq.h + 4 * lane), a.scale)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-    Row row;
-    if (a.prefix > 0)
-        take_keys(row, q, static_cast<const T *>(a.pk) + hk * a.spk.h + 4 * lane,
-                  static_cast<const T *>(a.pv) + hk * a.spv.h + 4 * lane, a.spk.t, a.spv.t, a.prefix, live);
-    const int64_t n = a.room > 0 ? min(max(int64_t(a.lens[b]), int64_t(0)), a.room) : 0;
-    if (n > 0)
-        take_keys(row, q, static_cast<const T *>(a.k) + b * a.k_batch + hk * a.sk.h + 4 * lane,
-                  static_cast<const T *>(a.v) + b * a.v_batch + hk * a.sv.h + 4 * lane, a.sk.t, a.sv.t, n, live);
-    finish(row, static_cast<T *>(a.out) + b * a.so.t + h * a.so.h + 4 * lane,
-           a.lse ? a.lse + b * a.shape.hq + h : nullptr, lane, live);
+template <typename T, int DP> cudaError_t launch_dp(const DecArgs &a, int64_t pairs, int ctas, cudaStream_t st) {
+    auto kern = attn_decode_kernel<T, DP>;
+    cudaError_t e = ensure_smem(kern, Ring<DP>::kBytes);
+    if (e != cudaSuccess) return e;
+    if (ctas > 8) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(pairs * ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ring<DP>::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ctas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    // after the tensor-core phase: start on SMs that it leaves free, and wait for it in the join
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.parts > 0 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace
 
-size_t attn_decode_workspace_bytes(const DecodeArgs &) { return 256; }
+size_t attn_decode_workspace_bytes(const DecodeArgs &d) {
+    if (!prefix_on_tensor_cores(d)) return 256;
+    const size_t splits = attn_prefix_splits(d), rows = size_t(d.batch) * d.shape.hq;
+    return 256 + align256(splits * rows * d.shape.d * 4) + align256(splits * rows * 4);
+}
 
-cudaError_t launch_attn_decode(const DecodeArgs &a, qmm_float t, void *ws, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(ws, 0, 16, st);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((a.batch + kRowWarps - 1) / kRowWarps), (unsigned)a.shape.hq);
-    if (t == QMM_F16) decode_rows_kernel<__half><<<grid, kRowWarps * 32, 0, st>>>(a);
-    else decode_rows_kernel<__nv_bfloat16><<<grid, kRowWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_attn_decode(const DecodeArgs &d, qmm_float t, void *ws, cudaStream_t st) {
+    DecArgs a{};
+    a.d = d;
+    a.group = d.shape.hq / d.shape.hk;
+    a.row_blocks = (a.group + kMaxRows - 1) / kMaxRows;
+    a.scale_log2 = d.scale * kLog2e;
+    a.status = static_cast<int *>(ws);
+    // maps that no tile uses describe q
+    const bool cache = d.room > 0, pre = d.prefix > 0;
+    if (!attn_make_map(&a.k, t, cache ? d.k : d.q, d.shape.d, cache ? d.shape.hk : 1, cache ? d.room : 1, d.sk, 1,
+                       kTileKeys, cache ? d.batch : 1, d.k_batch) ||
+        !attn_make_map(&a.v, t, cache ? d.v : d.q, d.shape.d, cache ? d.shape.hk : 1, cache ? d.room : 1, d.sv, 1,
+                       kTileKeys, cache ? d.batch : 1, d.v_batch))
+        return cudaErrorInvalidValue;
+    if (prefix_on_tensor_cores(d)) {
+        a.parts = attn_prefix_splits(d);
+        const size_t rows = size_t(d.batch) * d.shape.hq;
+        float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
+        float *lse = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256 +
+                                               align256(size_t(a.parts) * rows * d.shape.d * 4));
+        a.part = part;
+        a.part_lse = lse;
+        const cudaError_t e = launch_attn_prefix(d, t, a.parts, part, lse, ws, st);
+        if (e != cudaSuccess) return e;
+    } else if (pre) {
+        a.inline_prefix = d.prefix;
+        if (!attn_make_map(&a.pk, t, d.pk, d.shape.d, d.shape.hk, d.prefix, d.spk, 1, kTileKeys) ||
+            !attn_make_map(&a.pv, t, d.pv, d.shape.d, d.shape.hk, d.prefix, d.spv, 1, kTileKeys))
+            return cudaErrorInvalidValue;
+    }
+    const int64_t pairs = d.batch * d.shape.hk * a.row_blocks;
+    const int ctas = cluster_ctas(d, a.inline_prefix, pairs);
+    if (pairs * ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (t == QMM_F16) return d.shape.d <= 64 ? launch_dp<__half, 64>(a, pairs, ctas, st) : launch_dp<__half, 128>(a, pairs, ctas, st);
+    return d.shape.d <= 64 ? launch_dp<__nv_bfloat16, 64>(a, pairs, ctas, st)
+                           : launch_dp<__nv_bfloat16, 128>(a, pairs, ctas, st);
 }
 
 }  // namespace qmm

@@ -24,7 +24,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "qmm_attn.h"
+#include "qmm_attn.cuh"
 #include "qmm_internal.h"
 #include "qmm_tc_common.cuh"
 #include "qmm_tc_ptx.cuh"
@@ -39,7 +39,6 @@ constexpr int kRows = 128;    // rows of one half
 constexpr int kKeys = 128;    // keys of one tile
 constexpr int kTcThreads = 384;  // 168 registers each at launch: 64512 in all
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;  // 256 * 224 + 128 * 56 = 64512
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // how far (in powers of two) a row's scores may pass its maximum
 
 // Shared-memory plan for a padded head size DP: Q_0, Q_1, then a ring of K and V tiles.  A tile
@@ -52,10 +51,10 @@ template <int DP> struct Plan {
 
 struct TcArgs {
     CUtensorMap q, k, v;
-    void *out;              // direct output (splits == 1)
-    float *lse;             // [tokens][hq] natural log, or nullptr (splits == 1)
-    float *part;            // splits > 1: normalised fp32 partial rows [split][tokens * hq][d]
-    float *part_lse;        // their log2 denominators [split][tokens * hq]
+    void *out;              // direct output (part == nullptr)
+    float *lse;             // [tokens][hq] natural log, or nullptr (part == nullptr)
+    float *part;            // else normalised fp32 partial rows [split][tokens * hq][d]
+    float *part_lse;        // and their log2 denominators [split][tokens * hq]
     const void *v_data;     // V again, for the rare rows with non-finite values
     HeadStrides so, sv;
     HeadShape shape;
@@ -75,11 +74,6 @@ struct Item {
     int valid;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -96,12 +90,6 @@ __device__ __forceinline__ void add2(float &x, float &y, float a0, float a1) {
     asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nadd.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}"
         : "+f"(x), "+f"(y)
         : "f"(a0), "f"(a1));
-}
-template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    if (std::is_same<T, __half>::value) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 // The registers of earlier tensor-memory loads may be used from here on.
 template <int N> __device__ __forceinline__ void loaded(float (&v)[N]) {
@@ -227,6 +215,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     __shared__ int abort_s, odd_values;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (blockIdx.x == 0 && tid == 0) *a.status = QMM_OK;
+    grid_launch_dependents();  // a launch that waits for this one's end may take free SMs
 
     // blocks in order: all heads and splits of a tile, the last tiles (most keys) first
     int64_t rest = int64_t(gridDim.x) - 1 - blockIdx.x;
@@ -525,7 +514,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         }
                     }
                 }
-                if (a.splits == 1) {
+                if (!a.part) {
                     T *dst = static_cast<T *>(a.out) + (int64_t(it.q0) + t) * a.so.t + head * a.so.h + c * 32;
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
@@ -543,8 +532,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             }
             if (row_valid) {
                 const float l2 = none ? -INFINITY : top * a.scale_log2 + log2f(sum);
-                if (a.splits > 1) a.part_lse[int64_t(split) * a.tokens_q * a.shape.hq + row] = l2;
-                else if (a.lse) a.lse[row] = l2 * 0.6931471805599453f;
+                if (a.part) a.part_lse[int64_t(split) * a.tokens_q * a.shape.hq + row] = l2;
+                else if (a.lse) a.lse[row] = l2 * kLn2;
             }
         }
     }
@@ -555,56 +544,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// out[row] = sum_s 2^(lse_s - top) part_s[row] / sum_s 2^(lse_s - top); one warp a row.
-template <typename T>
-__global__ void __launch_bounds__(128) attn_join_kernel(const float *part, const float *part_lse, int parts,
-                                                        int64_t rows, HeadShape shape, T *out, HeadStrides so,
-                                                        float *lse) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= rows) return;
-    float top = -INFINITY;
-    for (int s = lane; s < parts; s += 32) top = fmaxf(top, part_lse[s * rows + row]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool live = 4 * lane < shape.d;
-    for (int s = 0; s < parts; ++s) {
-        const float l = part_lse[s * rows + row];
-        if (l == -INFINITY) continue;
-        const float w = ex2(l - base);
-        sum += w;
-        if (live) {
-            const float4 p = *reinterpret_cast<const float4 *>(part + (s * rows + row) * shape.d + 4 * lane);
-            acc.x += w * p.x;
-            acc.y += w * p.y;
-            acc.z += w * p.z;
-            acc.w += w * p.w;
-        }
-    }
-    const bool none = !(sum != 0.f);
-    const float inv = none ? 0.f : 1.f / sum;
-    const int64_t t = row / shape.hq;
-    const int h = int(row % shape.hq);
-    if (live)
-        *reinterpret_cast<uint2 *>(out + t * so.t + h * so.h + 4 * lane) =
-            make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
-    if (lse && lane == 0) lse[row] = none ? -INFINITY : (base + log2f(sum)) * 0.6931471805599453f;
-}
-
-// A [tokens][heads][d] view as a 3-dimensional map with boxes of 64 elements x heads x tokens.
-bool make_map(CUtensorMap *map, qmm_float t, const void *data, int d, int64_t heads, int64_t tokens, HeadStrides s,
-              int box_heads, int box_tokens) {
-    const uint64_t dims[3] = {uint64_t(d), uint64_t(heads), uint64_t(tokens)};
-    // a stride that is never taken still has to be a valid one
-    const uint64_t strides[2] = {uint64_t(heads > 1 ? s.h : d) * 2, uint64_t(tokens > 1 ? s.t : d) * 2};
-    const uint32_t box[3] = {64, uint32_t(box_heads), uint32_t(box_tokens)};
-    return tc_make_map(map, t == QMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, data,
-                       dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
-}
-
 template <typename T, int DP> cudaError_t launch_dp(const TcArgs &a, int64_t blocks, cudaStream_t st) {
     auto kern = attn_tc_kernel<T, DP>;
     cudaError_t e = ensure_smem(kern, Plan<DP>::kBytes);
@@ -613,78 +552,87 @@ template <typename T, int DP> cudaError_t launch_dp(const TcArgs &a, int64_t blo
     return cudaGetLastError();
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+// What the two launches have in common.
+TcArgs common_args(const HeadShape &shape, qmm_float t, float scale, void *ws) {
+    TcArgs a{};
+    a.shape = shape;
+    a.group = shape.hq / shape.hk;
+    a.per_half = kRows / a.group;
+    a.splits = 1;
+    // a scale of 0 (all keys alike) as the smallest one, so that a hidden key's -infinity stays one;
+    // a negative scale negates Q in the product
+    a.scale_log2 = std::max(std::abs(scale) * kLog2e, 1.2e-38f);
+    const uint32_t type_bits = t == QMM_F16 ? 0u : (1u << 7) | (1u << 10);
+    a.idesc_qk = idesc_f16_f32(kRows, kKeys) | type_bits | (scale < 0.f ? 1u << 13 : 0u);
+    a.idesc_pv = idesc_f16_f32(kRows, shape.d <= 64 ? 64 : 128) | type_bits | (1u << 16);
+    a.status = static_cast<int *>(ws);
+    return a;
+}
 
-int64_t prompt_tiles(const PromptArgs &a) {
-    const int64_t span = 2 * (kRows / (a.shape.hq / a.shape.hk));
-    // each sequence ends in at most one partial tile, and holds at least one token per tile
-    return std::min(a.tokens_q, a.tokens_q / span + (a.cu_q || a.n_seqs > 1 ? a.n_seqs : 1));
+cudaError_t launch_tc(const TcArgs &a, qmm_float t, int64_t blocks, cudaStream_t st) {
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (t == QMM_F16)
+        return a.shape.d <= 64 ? launch_dp<__half, 64>(a, blocks, st) : launch_dp<__half, 128>(a, blocks, st);
+    return a.shape.d <= 64 ? launch_dp<__nv_bfloat16, 64>(a, blocks, st)
+                           : launch_dp<__nv_bfloat16, 128>(a, blocks, st);
 }
 
 }  // namespace
 
-// Key splits of a prompt call: one, unless the tiles leave most SMs idle and the keys are many.
-int attn_prompt_splits(const PromptArgs &) { return 1; }
-
-size_t attn_prompt_workspace_bytes(const PromptArgs &a) {
-    const int splits = attn_prompt_splits(a);
-    if (splits == 1) return 256;
-    const size_t rows = size_t(a.tokens_q) * a.shape.hq;
-    return 256 + align256(size_t(splits) * rows * a.shape.d * 4) + align256(size_t(splits) * rows * 4);
-}
+size_t attn_prompt_workspace_bytes(const PromptArgs &) { return 256; }
 
 cudaError_t launch_attn_prompt(const PromptArgs &p, qmm_float t, void *ws, cudaStream_t st) {
-    TcArgs a{};
-    const int g = p.shape.hq / p.shape.hk, per_half = kRows / g;
-    if (!make_map(&a.q, t, p.q, p.shape.d, p.shape.hq, p.tokens_q, p.sq, g, per_half)) return cudaErrorInvalidValue;
+    TcArgs a = common_args(p.shape, t, p.scale, ws);
+    if (!attn_make_map(&a.q, t, p.q, p.shape.d, p.shape.hq, p.tokens_q, p.sq, a.group, a.per_half))
+        return cudaErrorInvalidValue;
     // without any key the maps are not used; they describe q then
     const bool keys = p.tokens_k > 0;
-    if (!make_map(&a.k, t, keys ? p.k : p.q, p.shape.d, keys ? p.shape.hk : 1, keys ? p.tokens_k : 1, p.sk, 1, kKeys) ||
-        !make_map(&a.v, t, keys ? p.v : p.q, p.shape.d, keys ? p.shape.hk : 1, keys ? p.tokens_k : 1, p.sv, 1, kKeys))
+    if (!attn_make_map(&a.k, t, keys ? p.k : p.q, p.shape.d, keys ? p.shape.hk : 1, keys ? p.tokens_k : 1, p.sk, 1, kKeys) ||
+        !attn_make_map(&a.v, t, keys ? p.v : p.q, p.shape.d, keys ? p.shape.hk : 1, keys ? p.tokens_k : 1, p.sv, 1, kKeys))
         return cudaErrorInvalidValue;
     a.out = p.out;
     a.lse = p.lse;
     a.v_data = p.v;
     a.so = p.so;
     a.sv = p.sv;
-    a.shape = p.shape;
     a.cu_q = p.cu_q;
     a.cu_k = p.cu_k;
     a.n_seqs = p.n_seqs;
     a.tokens_q = p.tokens_q;
     a.tokens_k = p.tokens_k;
-    a.group = g;
-    a.per_half = per_half;
     a.causal = p.causal;
-    a.splits = attn_prompt_splits(p);
-    // a scale of 0 (all keys alike) as the smallest one, so that a hidden key's -infinity stays one;
-    // a negative scale negates Q in the product
-    a.scale_log2 = std::max(std::abs(p.scale) * kLog2e, 1.2e-38f);
-    const int dp = p.shape.d <= 64 ? 64 : 128;
-    const uint32_t type_bits = t == QMM_F16 ? 0u : (1u << 7) | (1u << 10);
-    a.idesc_qk = idesc_f16_f32(kRows, kKeys) | type_bits | (p.scale < 0.f ? 1u << 13 : 0u);
-    a.idesc_pv = idesc_f16_f32(kRows, dp) | type_bits | (1u << 16);
-    a.status = static_cast<int *>(ws);
-    const int64_t rows = p.tokens_q * p.shape.hq;
-    if (a.splits > 1) {
-        a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256);
-        a.part_lse = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + 256 +
-                                               align256(size_t(a.splits) * rows * p.shape.d * 4));
-    }
-    const int64_t blocks = prompt_tiles(p) * a.splits * p.shape.hk;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    cudaError_t e;
-    if (t == QMM_F16) e = dp == 64 ? launch_dp<__half, 64>(a, blocks, st) : launch_dp<__half, 128>(a, blocks, st);
-    else e = dp == 64 ? launch_dp<__nv_bfloat16, 64>(a, blocks, st) : launch_dp<__nv_bfloat16, 128>(a, blocks, st);
-    if (e != cudaSuccess || a.splits == 1) return e;
-    const unsigned grid = (unsigned)((rows + 3) / 4);
-    if (t == QMM_F16)
-        attn_join_kernel<__half><<<grid, 128, 0, st>>>(a.part, a.part_lse, a.splits, rows, p.shape,
-                                                       static_cast<__half *>(p.out), p.so, p.lse);
-    else
-        attn_join_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a.part, a.part_lse, a.splits, rows, p.shape,
-                                                              static_cast<__nv_bfloat16 *>(p.out), p.so, p.lse);
-    return cudaGetLastError();
+    // each sequence ends in at most one partial tile, and every tile holds a token
+    const int64_t tiles = std::min(p.tokens_q, p.tokens_q / (2 * a.per_half) + p.n_seqs);
+    return launch_tc(a, t, tiles * p.shape.hk, st);
+}
+
+// The prefix's key splits: enough CTAs (tiles of queries x kv heads x splits) for every SM, at
+// least two key tiles each.
+int attn_prefix_splits(const DecodeArgs &d) {
+    const int64_t span = 2 * (kRows / (d.shape.hq / d.shape.hk));
+    const int64_t pairs = (d.batch + span - 1) / span * d.shape.hk, tiles = (d.prefix + kKeys - 1) / kKeys;
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>({device_sm_count() / pairs, tiles / 2, int64_t(kMaxPrefixParts)}));
+    const int64_t per = (tiles + most - 1) / most;
+    return int((tiles + per - 1) / per);
+}
+
+cudaError_t launch_attn_prefix(const DecodeArgs &d, qmm_float t, int splits, float *part, float *part_lse, void *ws,
+                               cudaStream_t st) {
+    TcArgs a = common_args(d.shape, t, d.scale, ws);
+    if (!attn_make_map(&a.q, t, d.q, d.shape.d, d.shape.hq, d.batch, d.sq, a.group, a.per_half) ||
+        !attn_make_map(&a.k, t, d.pk, d.shape.d, d.shape.hk, d.prefix, d.spk, 1, kKeys) ||
+        !attn_make_map(&a.v, t, d.pv, d.shape.d, d.shape.hk, d.prefix, d.spv, 1, kKeys))
+        return cudaErrorInvalidValue;
+    a.part = part;
+    a.part_lse = part_lse;
+    a.v_data = d.pv;
+    a.sv = d.spv;
+    a.n_seqs = 1;
+    a.tokens_q = d.batch;
+    a.tokens_k = d.prefix;
+    a.splits = splits;
+    const int64_t tiles = (d.batch + 2 * a.per_half - 1) / (2 * a.per_half);
+    return launch_tc(a, t, tiles * splits * d.shape.hk, st);
 }
 
 }  // namespace qmm
