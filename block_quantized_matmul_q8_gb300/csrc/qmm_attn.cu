@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "qmm_attn.cuh"
 #include "qmm_internal.h"
@@ -32,12 +33,15 @@ constexpr int kMaxRows = 16;           // query heads of one CTA
 constexpr int kMaxCluster = 16;
 
 template <int DP> struct Ring {
-    static constexpr int kHalf = kTileKeys * DP * 2;  // a K or a V tile: DP/64 blocks of 64 x 128 bytes
-    static constexpr int kStages = DP == 128 ? 3 : 6;
+    // Stages hold a K tile or a V tile by turns: DP/64 blocks of 64 x 128 bytes.  64 KB of them and
+    // 128 registers a thread let three CTAs share an SM, so that one's start and join overlap the
+    // others' copies.
+    static constexpr int kTile = kTileKeys * DP * 2;
+    static constexpr int kStages = DP == 128 ? 4 : 8;
     static constexpr int kPartStride = DP + 4;        // floats between a warp's partial rows
-    static constexpr size_t kBytes = size_t(2 * kStages) * kHalf + 1024;
+    static constexpr size_t kBytes = size_t(kStages) * kTile + 1024;
     static constexpr int kParts = kWarps * kMaxRows * kPartStride;  // floats of the CTA's partial rows
-    static_assert((kParts + kMaxRows * (kMaxCluster * kWarps + kMaxPrefixParts + 2)) * 4 <= 2 * kStages * kHalf,
+    static_assert((kParts + kMaxRows * (kMaxCluster + kMaxPrefixParts + 2)) * 4 <= kStages * kTile,
                   "partial rows and weights reuse the ring");
 };
 
@@ -106,31 +110,31 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ float peer_f32(uint32_t addr, uint32_t rank) {
     uint32_t p;
     float v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(p));
     return v;
 }
 __device__ __forceinline__ float4 peer_f32x4(uint32_t addr, uint32_t rank) {
     uint32_t p;
     float4 v;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(p)
-                 : "memory");
+                 : "r"(p));
     return v;
 }
 
 // Byte of 16-byte unit u of a row in a block of rows of 128 bytes, 128-byte swizzled.
 __device__ __forceinline__ uint32_t swizzled(int row, int u) { return uint32_t(row * 128 + ((u ^ (row & 7)) << 4)); }
 
-template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_constant__ DecArgs a) {
+template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 3) attn_decode_kernel(const __grid_constant__ DecArgs a) {
     using R = Ring<DP>;
     constexpr int ST = R::kStages, KS = DP / 16;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[ST], empty[ST];
     __shared__ int abort_s;
     __shared__ float ml_s[kWarps][kMaxRows][2];  // each warp's maximum and sum (log2 domain)
+    __shared__ float joined_s[kMaxRows][2];      // the CTA's
     const DecodeArgs &d = a.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
@@ -157,6 +161,14 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_d
         }
         fence_mbar_init();
     }
+    if (warp == kWarps && lane == 0) {
+        prefetch_tmap(&a.k);
+        prefetch_tmap(&a.v);
+        if (ptiles > 0) {
+            prefetch_tmap(&a.pk);
+            prefetch_tmap(&a.pv);
+        }
+    }
     __syncthreads();
     volatile int *abort = &abort_s;
 
@@ -165,21 +177,19 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_d
         bool ok = true;
         int issued = 0;
         if (lane == 0) {
-            for (int i = 0; i < n && ok; ++i) {
-                const int stg = i % ST;
+            for (int i = 0; i < 2 * n && ok; ++i) {
+                const int stg = i % ST, kv = i & 1;
                 if (i >= ST) ok = mbar_wait(smem_u32(&empty[stg]), ((i / ST) - 1) & 1, abort);
                 if (!ok) break;
-                const uint32_t bar = smem_u32(&full[stg]), dst = sm + stg * 2 * R::kHalf;
-                mbar_arrive_expect_tx(bar, 2 * R::kHalf);
-                const int64_t j = j0 + i;
+                const uint32_t bar = smem_u32(&full[stg]), dst = sm + stg * R::kTile;
+                mbar_arrive_expect_tx(bar, R::kTile);
+                const int64_t j = j0 + (i >> 1);
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-                    for (int c = 0; c < DP / 64; ++c) {
-                        const uint32_t to = dst + kv * R::kHalf + c * kTileKeys * 128;
-                        if (j < ptiles) tma_load_3d(to, kv ? &a.pv : &a.pk, c * 64, hk, int(j * kTileKeys), bar);
-                        else tma_load_4d(to, kv ? &a.v : &a.k, c * 64, hk, int((j - ptiles) * kTileKeys), int(b), bar);
-                    }
+                for (int c = 0; c < DP / 64; ++c) {
+                    const uint32_t to = dst + c * kTileKeys * 128;
+                    if (j < ptiles) tma_load_3d(to, kv ? &a.pv : &a.pk, c * 64, hk, int(j * kTileKeys), bar);
+                    else tma_load_4d(to, kv ? &a.v : &a.k, c * 64, hk, int((j - ptiles) * kTileKeys), int(b), bar);
+                }
                 issued = i + 1;
             }
             if (!ok)  // a wait gave up: the copies in flight land before the ring is reused or released
@@ -210,22 +220,14 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_d
                 }
         }
         for (int i = 0; i < n; ++i) {
-            const int stg = i % ST;
-            if (!mbar_wait(smem_u32(&full[stg]), (i / ST) & 1, abort)) break;
+            const int k_stg = (2 * i) % ST, v_stg = k_stg + 1, phase = ((2 * i) / ST) & 1;
+            const uint32_t kt = sm + k_stg * R::kTile, vt = kt + R::kTile;
+            if (!warp_wait(smem_u32(&full[k_stg]), phase, abort)) break;
             const int64_t j = j0 + i;
             const int64_t left = j < ptiles ? a.inline_prefix - j * kTileKeys : len - (j - ptiles) * kTileKeys;
             const int valid = int(min(left, int64_t(kTileKeys))) - warp * 16;  // of this warp's keys
+            uint32_t p[4];
             if (valid > 0) {
-                const uint32_t kt = sm + stg * 2 * R::kHalf, vt = kt + R::kHalf;
-                if (valid < 16) {
-                    // rows that nobody owns may hold anything: zero weights times them must be zero
-                    uint8_t *v = raw + (vt - smem_u32(raw));
-                    for (int c = 0; c < DP / 64; ++c)
-                        for (int u = valid * 8 + lane; u < 16 * 8; u += 32)
-                            reinterpret_cast<uint4 *>(v + c * kTileKeys * 128 + warp * 16 * 128)[u] = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
                 float s[2][4] = {};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
@@ -263,7 +265,6 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_d
                         }
                     }
                 }
-                uint32_t p[4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float base = top[h] == -INFINITY ? 0.f : top[h];
@@ -273,6 +274,20 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_d
                         sum[h] += x + y;
                         p[t * 2 + h] = pack2<T>(x, y);
                     }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&empty[k_stg]));
+            if (!warp_wait(smem_u32(&full[v_stg]), phase, abort)) break;
+            if (valid > 0) {
+                if (valid < 16) {
+                    // rows that nobody owns may hold anything: zero weights times them must be zero
+                    uint8_t *v = raw + (vt - smem_u32(raw));
+                    for (int c = 0; c < DP / 64; ++c)
+                        for (int u = valid * 8 + lane; u < 16 * 8; u += 32)
+                            reinterpret_cast<uint4 *>(v + c * kTileKeys * 128 + warp * 16 * 128)[u] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
                 }
 #pragma unroll
                 for (int c = 0; c < DP / 16; ++c) {
@@ -284,7 +299,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_d
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&empty[stg]));
+            if (lane == 0) mbar_arrive(smem_u32(&empty[v_stg]));
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -294,8 +309,8 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_d
     }
     __syncthreads();  // the ring is free: every copy was waited for
     float *part = reinterpret_cast<float *>(raw + (sm - smem_u32(raw)));
-    // weights of the partial rows in the join: this request's warps and the tensor-core phase's splits
-    auto weight_s = reinterpret_cast<float(*)[kMaxCluster * kWarps + 1]>(part + R::kParts);
+    // weights of the partial rows in the join: the cluster's CTAs and the tensor-core phase's splits
+    auto weight_s = reinterpret_cast<float(*)[kMaxCluster + 1]>(part + R::kParts);
     auto pweight_s = reinterpret_cast<float(*)[kMaxPrefixParts + 1]>(weight_s + kMaxRows);
     if (warp < kWarps) {
 #pragma unroll
@@ -303,88 +318,103 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads) attn_d
             const int row = (lane >> 2) + 8 * h;
             if (row >= rows) continue;
             float *dst = part + (warp * kMaxRows + row) * R::kPartStride + (lane & 3) * 2;
-            if (n > 0)
 #pragma unroll
-                for (int c = 0; c < DP / 8; ++c)
-                    *reinterpret_cast<float2 *>(dst + c * 8) = make_float2(o[c][2 * h], o[c][2 * h + 1]);
+            for (int c = 0; c < DP / 8; ++c)
+                *reinterpret_cast<float2 *>(dst + c * 8) = make_float2(o[c][2 * h], o[c][2 * h + 1]);
             if ((lane & 3) == 0) {
                 ml_s[warp][row][0] = top[h];
                 ml_s[warp][row][1] = sum[h];
             }
         }
     }
-    cluster_sync();
+    __syncthreads();
+    // the warps' rows joined into the first warp's
+    const int quads = d.shape.d / 4;
+    for (int e = tid; e < rows * quads; e += kThreads) {
+        const int row = e / quads, col = (e - row * quads) * 4;
+        float m[kWarps], most = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) most = fmaxf(most, m[w] = ml_s[w][row][0]);
+        const float base = most == -INFINITY ? 0.f : most;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float total = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2(m[w] - base);
+            const float4 x = *reinterpret_cast<const float4 *>(part + (w * kMaxRows + row) * R::kPartStride + col);
+            acc.x += f * x.x;
+            acc.y += f * x.y;
+            acc.z += f * x.z;
+            acc.w += f * x.w;
+            total += f * ml_s[w][row][1];
+        }
+        *reinterpret_cast<float4 *>(part + row * R::kPartStride + col) = acc;
+        if (col == 0) {
+            joined_s[row][0] = most;
+            joined_s[row][1] = total;
+        }
+    }
+    if (ranks > 1) cluster_sync();
+    else __syncthreads();
     if (*abort && tid == 0) *a.status = QMM_ERR_DEVICE;
 
     // ------------------------------------------------ the join
     if (a.parts > 0) grid_dependency_wait();
-    const int own = ranks * kWarps;
     const int64_t row0 = b * d.shape.hq + head0, all_rows = d.batch * d.shape.hq;
     for (int row = warp; row < rows; row += kWarps + 1) {
-        float most = -INFINITY;
-        for (int p = lane; p < own; p += 32) {
-            const float m = peer_f32(smem_u32(&ml_s[p & (kWarps - 1)][row][0]), p / kWarps);
-            weight_s[row][p] = m;
-            most = fmaxf(most, m);
+        float m = -INFINITY, l = 0.f, most;
+        if (ranks == 1) {
+            m = lane == 0 ? joined_s[row][0] : m;
+            l = lane == 0 ? joined_s[row][1] : l;
+        } else if (lane < ranks) {
+            m = peer_f32(smem_u32(&joined_s[row][0]), lane);
+            l = peer_f32(smem_u32(&joined_s[row][1]), lane);
         }
+        most = m;
         for (int p = lane; p < a.parts; p += 32) {
-            const float m = a.part_lse[p * all_rows + row0 + row];
-            pweight_s[row][p] = m;
-            most = fmaxf(most, m);
+            const float x = a.part_lse[p * all_rows + row0 + row];
+            pweight_s[row][p] = x;
+            most = fmaxf(most, x);
         }
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
         const float base = most == -INFINITY ? 0.f : most;
-        float total = 0.f;
-        for (int p = lane; p < own; p += 32) {
-            const float l = peer_f32(smem_u32(&ml_s[p & (kWarps - 1)][row][1]), p / kWarps);
-            const float m = weight_s[row][p];
-            const float w = m == -INFINITY && l == 0.f ? 0.f : ex2(m - base);  // 0: no key
-            weight_s[row][p] = w;
-            total += w * l;
-        }
-        for (int p = lane; p < a.parts; p += 32) {
-            const float m = pweight_s[row][p], w = m == -INFINITY ? 0.f : ex2(m - base);
-            pweight_s[row][p] = w;
-            total += w;
-        }
+        const float w = ex2(m - base);
+        float total = w * l;
+        for (int p = lane; p < a.parts; p += 32) total += pweight_s[row][p] = ex2(pweight_s[row][p] - base);
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) total += __shfl_xor_sync(0xffffffffu, total, s);
         const bool none = !(total != 0.f);
         const float inv = none ? 0.f : 1.f / total;
-        for (int p = lane; p < own; p += 32) weight_s[row][p] *= inv;
+        if (lane < ranks) weight_s[row][lane] = w * inv;
         for (int p = lane; p < a.parts; p += 32) pweight_s[row][p] *= inv;
         if (d.lse && lane == 0 && rank == 0) d.lse[row0 + row] = none ? -INFINITY : (base + log2f(total)) * kLn2;
     }
     __syncthreads();
-    const int quads = d.shape.d / 4;
-    for (int e = rank * kThreads + tid; e < rows * quads; e += ranks * kThreads) {
+    for (int e = rank + tid * ranks; e < rows * quads; e += ranks * kThreads) {
         const int row = e / quads, col = (e - row * quads) * 4;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < own; ++p) {
-            const float w = weight_s[row][p];
-            if (w == 0.f) continue;
-            const float4 x = peer_f32x4(
-                smem_u32(part + ((p & (kWarps - 1)) * kMaxRows + row) * R::kPartStride + col), p / kWarps);
+        auto add = [&](float w, float4 x) {
             acc.x += w * x.x;
             acc.y += w * x.y;
             acc.z += w * x.z;
             acc.w += w * x.w;
+        };
+        const uint32_t addr = smem_u32(part + row * R::kPartStride + col);
+        if (ranks == 1) {
+            add(weight_s[row][0], *reinterpret_cast<const float4 *>(part + row * R::kPartStride + col));
+        } else {
+#pragma unroll 4
+            for (int p = 0; p < ranks; ++p) add(weight_s[row][p], peer_f32x4(addr, p));
         }
-        for (int p = 0; p < a.parts; ++p) {
-            const float w = pweight_s[row][p];
-            if (w == 0.f) continue;
-            const float4 x =
-                *reinterpret_cast<const float4 *>(a.part + (p * all_rows + row0 + row) * d.shape.d + col);
-            acc.x += w * x.x;
-            acc.y += w * x.y;
-            acc.z += w * x.z;
-            acc.w += w * x.w;
-        }
+        const float *src = a.part + (row0 + row) * d.shape.d + col;
+        const int64_t step = all_rows * d.shape.d;
+#pragma unroll 4
+        for (int p = 0; p < a.parts; ++p) add(pweight_s[row][p], __ldcg(reinterpret_cast<const float4 *>(src + p * step)));
         T *out = static_cast<T *>(d.out) + b * d.so.t + (head0 + row) * d.so.h + col;
         *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
     }
-    cluster_sync();  // no CTA leaves while its shared memory may be read
+    if (ranks > 1) cluster_sync();  // no CTA leaves while its shared memory may be read
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -392,6 +422,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // Whether the prefix goes through the tensor-core phase: the rows of the batch that share a kv
 // head are many enough that reading the prefix once for all of them pays for a second launch.
 bool prefix_on_tensor_cores(const DecodeArgs &d) {
+    if (getenv("X_TC")) return d.prefix > 0 && atoi(getenv("X_TC"));
     return d.prefix > 0 && d.batch * d.prefix > 16384;
 }
 
@@ -399,6 +430,7 @@ bool prefix_on_tensor_cores(const DecodeArgs &d) {
 int cluster_ctas(const DecodeArgs &d, int64_t inline_prefix, int64_t pairs) {
     const int64_t tiles = (inline_prefix + kTileKeys - 1) / kTileKeys + (d.room + kTileKeys - 1) / kTileKeys;
     int c = 1;
+    if (getenv("X_C")) return atoi(getenv("X_C"));
     while (c < kMaxCluster && pairs * c < 6 * device_sm_count() && tiles >= 2 * c) c *= 2;
     return c;
 }

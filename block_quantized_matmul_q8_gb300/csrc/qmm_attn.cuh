@@ -8,6 +8,7 @@
 
 #include "qmm_attn.h"
 #include "qmm_tc_common.cuh"
+#include "qmm_tc_ptx.cuh"
 
 namespace qmm {
 
@@ -25,6 +26,11 @@ template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float 
     else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// mbar_wait by a whole warp: all lanes go on, or all give up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort));
+}
+
 // A [tokens][heads][d] view (batch of them: batch_stride elements apart) as a tensor map with
 // boxes of 64 elements x box_heads x box_tokens, 128-byte swizzled.  A stride that is never
 // taken is given as one that the encoder accepts.

@@ -12,8 +12,9 @@
 // the other half's two products.  A row's maximum is only moved when it grows by more than 2^8
 // (weights then stay below 256, exact in the fp32 sums), so O_i is rarely rescaled.
 //
-// Warps: 0-3 and 4-7 softmax of half 0 and 1, 8 TMA copies, 9 MMA issue (10 and 11 only fill up
-// their warpgroup, which gives its registers to the softmax ones).
+// Warps: 0-3 and 4-7 softmax of half 0 and 1, 8 TMA copies, 9 MMA issue (one issuer keeps the
+// halves in turn; with one each they fall into step and the tensor cores idle), 10 and 11 only
+// fill up their warpgroup, which gives its registers to the softmax ones.
 // Bounds: at large sizes the tensor pipe and the exponentials (128 x 128 per 2 x 128x128xD
 // products) take about the same time; at small ones the start of the CTA (copy latency).
 #include <cuda.h>
@@ -22,6 +23,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <type_traits>
 
 #include "qmm_attn.cuh"
@@ -112,6 +114,17 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t lbo_byt
            (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+// One lane of the converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
+    return yes != 0;
+}
+// mbar_wait_spin by a whole warp: all lanes go on, or all give up.
+__device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, abort));
+}
+
 // Clamped [cu[s], cu[s + 1]) as (first, length).
 __device__ __forceinline__ void seq_bounds(const int32_t *cu, int64_t s, int64_t most, int &first, int &len) {
     const int64_t a = min(max(int64_t(cu[s]), int64_t(0)), most), b = min(max(int64_t(cu[s + 1]), int64_t(0)), most);
@@ -200,8 +213,14 @@ template <typename T, int DP> __device__ __forceinline__ bool clean_values(uint8
     return __any_sync(0xffffffffu, seen != 0);
 }
 
+// Stages are released in pairs, (V_j, K_{j+1}) after K_0 alone, by the softmax threads: a half's
+// scores S(j+1) are complete after its products on both.  No half gets as many as kReleases pairs
+// ahead of the other: the ring holds at most 5 pairs, and the halves' numbers of tiles differ by
+// at most 2.
+constexpr int kReleases = 16;
+
 struct Bars {
-    uint64_t q, full[8], empty[8], clean[8], s[2], p[2], o[2], drain;
+    uint64_t q, full[8], clean[8], empty[kReleases], s[2], p[2][2], o[2], drain;
 };
 
 template <typename T, int DP>
@@ -234,12 +253,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             mbar_init(smem_u32(&bars.q), 1);
             for (int i = 0; i < ST; ++i) {
                 mbar_init(smem_u32(&bars.full[i]), 1);
-                mbar_init(smem_u32(&bars.empty[i]), 1);
                 mbar_init(smem_u32(&bars.clean[i]), 1);
             }
+            const bool two_halves = it.t0 + a.per_half < it.lq;
+            for (int i = 0; i < kReleases; ++i) mbar_init(smem_u32(&bars.empty[i]), two_halves ? 2 : 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_u32(&bars.s[i]), 1);
-                mbar_init(smem_u32(&bars.p[i]), 4);
+                mbar_init(smem_u32(&bars.p[i][0]), 4);
+                mbar_init(smem_u32(&bars.p[i][1]), 4);
                 mbar_init(smem_u32(&bars.o[i]), 1);
             }
             mbar_init(smem_u32(&bars.drain), 1);
@@ -264,6 +285,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 
     // key tiles [ja, jb[i]) of each half; vis_lo: the keys that every row of the CTA sees
     const int half_tokens = a.per_half;
+    const bool two_halves = it.t0 + half_tokens < it.lq;
     const int vis_lo = visible(a, it, it.t0);
     int n[2];
 #pragma unroll
@@ -288,7 +310,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         auto clean = [&](int j) {
             if ((j + 1) * kKeys <= vis_lo) return;
             const int item = 2 * (j - ja) + 1, stg = item % ST;
-            ok = mbar_wait(smem_u32(&bars.full[stg]), (item / ST) & 1, abort);
+            ok = warp_wait(smem_u32(&bars.full[stg]), (item / ST) & 1, abort);
             if (!ok) return;
             const bool odd = clean_values<T, DP>(raw + (sm0 - smem_u32(raw)) + (2 + stg) * P::kTile,
                                                  max(vis_lo - j * kKeys, 0), min(it.lk - j * kKeys, kKeys), lane);
@@ -314,7 +336,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (int j = ja; j < jb && ok; ++j) {
             for (int kv = 0; kv < 2 && ok; ++kv) {
                 const int item = 2 * (j - ja) + kv, stg = item % ST;
-                if (item >= ST) ok = mbar_wait(smem_u32(&bars.empty[stg]), ((item / ST) - 1) & 1, abort);
+                if (item >= ST) {
+                    const int pair = (item - ST + 1) / 2;
+                    ok = warp_wait(smem_u32(&bars.empty[pair % kReleases]), (pair / kReleases) & 1, abort);
+                }
                 if (ok && lane == 0) {
                     const uint32_t bar = smem_u32(&bars.full[stg]);
                     mbar_arrive_expect_tx(bar, P::kTile);
@@ -331,64 +356,70 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         if (ok && jb > ja) clean(jb - 1);
         if (!ok) {  // a wait gave up: the copies in flight land before shared memory is released
             int never = 0;
-            mbar_wait(smem_u32(&bars.q), 0, &never);
+            warp_wait(smem_u32(&bars.q), 0, &never);
             for (int item = max(issued - ST, 0); item < issued; ++item) {
                 never = 0;
-                mbar_wait(smem_u32(&bars.full[item % ST]), (item / ST) & 1, &never);
+                warp_wait(smem_u32(&bars.full[item % ST]), (item / ST) & 1, &never);
             }
         }
     } else if (warp == 9) {
-        // ------------------------------------------------ products
-        if (lane == 0 && jb > ja) {
-            bool ok = mbar_wait_spin(smem_u32(&bars.q), 0, abort);
+        // ------------------------------------------------ products, issued by one elected lane
+        if (jb > ja) {
+            bool ok = spin_wait(smem_u32(&bars.q), 0, abort);
             auto full = [&](int item) {
-                ok = ok && mbar_wait_spin(smem_u32(&bars.full[item % ST]), (item / ST) & 1, abort);
+                ok = ok && spin_wait(smem_u32(&bars.full[item % ST]), (item / ST) & 1, abort);
             };
-            auto qk = [&](int i, int j) {
-                const uint32_t kt = skv + uint32_t((2 * (j - ja)) % ST) * P::kTile, qt = sq + i * P::kTile;
+            const uint64_t qd = smem_desc(sq, 1024, 2);
+            auto qk = [&](int i, int item) {
+                const uint64_t kd = smem_desc(skv + uint32_t(item % ST) * P::kTile, 1024, 2);
+                if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < DP / 16; ++s) {
-                    const uint32_t off = uint32_t(s / 4) * kRows * 128 + uint32_t(s % 4) * 32;
-                    mma_f16(tmem + i * kKeys, smem_desc(qt + off, 1024, 2), smem_desc(kt + off, 1024, 2), a.idesc_qk,
-                            s != 0);
+                    for (int s = 0; s < DP / 16; ++s) {
+                        const uint32_t off = (uint32_t(s / 4) * kRows * 128 + uint32_t(s % 4) * 32) >> 4;
+                        mma_f16(tmem + i * kKeys, qd + uint32_t(i * P::kTile >> 4) + off, kd + off, a.idesc_qk, s != 0);
+                    }
+                    mma_commit(smem_u32(&bars.s[i]));
                 }
-                mma_commit(smem_u32(&bars.s[i]));
+                __syncwarp();
             };
             full(0);
             tc_fence_after();
-            if (ok && jb0 > ja) qk(0, ja);
-            if (ok && jb1 > ja) qk(1, ja);
-            if (ok) mma_commit(smem_u32(&bars.empty[0]));
+            if (ok && jb0 > ja) qk(0, 0);
+            if (ok && jb1 > ja) qk(1, 0);
             for (int j = ja; j < jb && ok; ++j) {
-                const int vi = 2 * (j - ja) + 1, ki = vi + 1;
-                const uint32_t vt = skv + uint32_t(vi % ST) * P::kTile;
+                const int vi = 2 * (j - ja) + 1;
+                // everything but the weights is normally there long before them
                 full(vi);
-                if (ok && (j + 1) * kKeys > vis_lo) ok = mbar_wait_spin(smem_u32(&bars.clean[vi % ST]), 0, abort);
+                if (ok && (j + 1) * kKeys > vis_lo) ok = spin_wait(smem_u32(&bars.clean[vi % ST]), 0, abort);
+                if (j + 1 < jb) full(vi + 1);
+                const uint64_t vd = smem_desc_mn(skv + uint32_t(vi % ST) * P::kTile, kKeys * 128);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int end = i ? jb1 : jb0;
-                    if (j >= end || !ok) continue;
-                    ok = mbar_wait_spin(smem_u32(&bars.p[i]), (j - ja) & 1, abort);
-                    if (!ok) continue;
-                    tc_fence_after();
+                    if (j >= end) continue;
 #pragma unroll
-                    for (int s = 0; s < kKeys / 16; ++s)
-                        mma_f16_tmem_a(tmem + 256 + i * DP, tmem + i * kKeys + s * 8,
-                                       smem_desc_mn(vt + s * 16 * 128, kKeys * 128), a.idesc_pv, j > ja || s > 0);
-                    if (j + 1 < end) {
-                        full(ki);
-                        if (ok) qk(i, j + 1);
-                    } else {
-                        mma_commit(smem_u32(&bars.o[i]));
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && spin_wait(smem_u32(&bars.p[i][h]), (j - ja) & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int s = h * 4; s < h * 4 + 4; ++s)
+                                mma_f16_tmem_a(tmem + 256 + i * DP, tmem + i * kKeys + s * 8,
+                                               vd + uint32_t(s * 16 * 128 >> 4), a.idesc_pv, j > ja || s > 0);
+                        }
+                        __syncwarp();
                     }
+                    if (!ok) break;
+                    if (j + 1 < end) qk(i, vi + 1);
+                    else if (elect_one()) mma_commit(smem_u32(&bars.o[i]));
+                    __syncwarp();
                 }
-                if (ok) mma_commit(smem_u32(&bars.empty[vi % ST]));
-                if (ok && j + 1 < jb) mma_commit(smem_u32(&bars.empty[ki % ST]));
             }
             if (!ok) {  // let what was issued end before the tensor memory is freed
-                mma_commit(smem_u32(&bars.drain));
+                if (elect_one()) mma_commit(smem_u32(&bars.drain));
                 int never = 0;
-                mbar_wait_spin(smem_u32(&bars.drain), 0, &never);
+                spin_wait(smem_u32(&bars.drain), 0, &never);
             }
         }
     }
@@ -406,8 +437,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         float top = -INFINITY, sum0 = 0.f, sum1 = 0.f;
         bool ok = true;
         for (int j = ja; j < end; ++j) {
-            ok = mbar_wait(smem_u32(&bars.s[i]), (j - ja) & 1, abort);
+            ok = warp_wait(smem_u32(&bars.s[i]), (j - ja) & 1, abort);
             if (!ok) break;
+            if ((tid & 127) == 0) mbar_arrive(smem_u32(&bars.empty[(j - ja) % kReleases]));
             tc_fence_after();
             float s[kKeys];
 #pragma unroll
@@ -466,11 +498,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     p[e] = pack2<T>(s[x], s[x + 1]);
                 }
                 tmem_st_32x32b_x16(s_addr + c * 16, p);
+                if (c & 1) {  // half of the keys: their product may begin
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.p[i][c >> 1]));
+                }
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.p[i]));
             // the row's sum, of the unrounded weights, while the product runs
             float a0 = s[0], a1 = s[1], b0 = s[2], b1 = s[3];
 #pragma unroll
@@ -481,7 +515,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             add2(a0, a1, b0, b1);
             add2(sum0, sum1, a0, a1);
         }
-        if (ok && end > ja) ok = mbar_wait(smem_u32(&bars.o[i]), 0, abort);
+        if ((tid & 127) == 0 && (i == 0 || two_halves))  // tiles that only the other half takes
+            for (int j = end; j < jb; ++j) mbar_arrive(smem_u32(&bars.empty[(j - ja) % kReleases]));
+        if (ok && end > ja) ok = warp_wait(smem_u32(&bars.o[i]), 0, abort);
         if (ok) {
             tc_fence_after();
             const float sum = end > ja ? sum0 + sum1 : 0.f;
@@ -612,6 +648,7 @@ int attn_prefix_splits(const DecodeArgs &d) {
     const int64_t span = 2 * (kRows / (d.shape.hq / d.shape.hk));
     const int64_t pairs = (d.batch + span - 1) / span * d.shape.hk, tiles = (d.prefix + kKeys - 1) / kKeys;
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>({device_sm_count() / pairs, tiles / 2, int64_t(kMaxPrefixParts)}));
+    if (getenv("X_S")) return std::min<int64_t>(tiles, atoi(getenv("X_S")));
     const int64_t per = (tiles + most - 1) / most;
     return int((tiles + per - 1) / per);
 }
