@@ -218,6 +218,7 @@ template <typename T, int DP> __device__ __forceinline__ bool clean_values(uint8
 // ahead of the other: the ring holds at most 5 pairs, and the halves' numbers of tiles differ by
 // at most 2.
 constexpr int kReleases = 16;
+constexpr int kParts = 2;  // parts of a tile's weights that are handed over one by one
 
 struct Bars {
     uint64_t q, full[8], clean[8], empty[kReleases], s[2], p[2][2], o[2], drain;
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             for (int i = 0; i < kReleases; ++i) mbar_init(smem_u32(&bars.empty[i]), two_halves ? 2 : 1);
             for (int i = 0; i < 2; ++i) {
                 mbar_init(smem_u32(&bars.s[i]), 1);
-                mbar_init(smem_u32(&bars.p[i][0]), 4);
+                mbar_init(smem_u32(&bars.p[i][0]), 5);
                 mbar_init(smem_u32(&bars.p[i][1]), 4);
                 mbar_init(smem_u32(&bars.o[i]), 1);
             }
@@ -386,40 +387,51 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             tc_fence_after();
             if (ok && jb0 > ja) qk(0, 0);
             if (ok && jb1 > ja) qk(1, 0);
-            for (int j = ja; j < jb && ok; ++j) {
-                const int vi = 2 * (j - ja) + 1;
-                // everything but the weights is normally there long before them
-                full(vi);
-                if (ok && (j + 1) * kKeys > vis_lo) ok = spin_wait(smem_u32(&bars.clean[vi % ST]), 0, abort);
-                if (j + 1 < jb) full(vi + 1);
-                const uint64_t vd = smem_desc_mn(skv + uint32_t(vi % ST) * P::kTile, kKeys * 128);
+            const uint64_t vd0 = smem_desc_mn(skv, kKeys * 128);
+#pragma unroll 1
+            for (int turn = 0; ok && turn < 2 * (jb - ja); ++turn) {
+                const int i = turn & 1, j = turn >> 1, left = (i ? jb1 : jb0) - ja - j;
+                if (left <= 0) continue;
+                const int vi = 2 * j + 1;
+                const uint64_t vd = vd0 + uint32_t((vi % ST) * P::kTile >> 4);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int end = i ? jb1 : jb0;
-                    if (j >= end) continue;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        ok = ok && spin_wait(smem_u32(&bars.p[i][h]), (j - ja) & 1, abort);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-#pragma unroll
-                            for (int s = h * 4; s < h * 4 + 4; ++s)
-                                mma_f16_tmem_a(tmem + 256 + i * DP, tmem + i * kKeys + s * 8,
-                                               vd + uint32_t(s * 16 * 128 >> 4), a.idesc_pv, j > ja || s > 0);
-                        }
-                        __syncwarp();
-                    }
+                for (int h = 0; h < kParts; ++h) {
+                    ok = ok && spin_wait(smem_u32(&bars.p[i][h]), j & 1, abort);
                     if (!ok) break;
-                    if (j + 1 < end) qk(i, vi + 1);
-                    else if (elect_one()) mma_commit(smem_u32(&bars.o[i]));
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = h * 8 / kParts; s < (h + 1) * 8 / kParts; ++s)
+                            mma_f16_tmem_a(tmem + 256 + i * DP, tmem + i * kKeys + s * 8,
+                                           vd + uint32_t(s * 16 * 128 >> 4), a.idesc_pv, j > 0 || s > 0);
+                    }
                     __syncwarp();
                 }
+                if (!ok) break;
+                if (left > 1) qk(i, vi + 1);
+                else if (elect_one()) mma_commit(smem_u32(&bars.o[i]));
+                __syncwarp();
             }
             if (!ok) {  // let what was issued end before the tensor memory is freed
                 if (elect_one()) mma_commit(smem_u32(&bars.drain));
                 int never = 0;
                 spin_wait(smem_u32(&bars.drain), 0, &never);
+            }
+        }
+    } else if (warp == 10 && lane == 0) {
+        // ------------------------------------------------ gate: V_j and K_{j+1} have arrived
+        // One arrival of each half's P barrier, so that the issuer waits for nothing else.
+        bool ok = true;
+        for (int j = ja; j < jb && ok; ++j) {
+            const int vi = 2 * (j - ja) + 1;
+            ok = mbar_wait(smem_u32(&bars.full[vi % ST]), (vi / ST) & 1, abort);
+            if (ok && (j + 1) * kKeys > vis_lo) ok = mbar_wait(smem_u32(&bars.clean[vi % ST]), 0, abort);
+            if (ok && j + 1 < jb)
+                ok = mbar_wait(smem_u32(&bars.full[(vi + 1) % ST]), ((vi + 1) / ST) & 1, abort);
+            for (int i = 0; i < 2 && ok; ++i) {
+                if (j >= (i ? jb1 : jb0)) continue;
+                if (j > ja) ok = mbar_wait(smem_u32(&bars.p[i][0]), (j - ja - 1) & 1, abort);
+                if (ok) mbar_arrive(smem_u32(&bars.p[i][0]));
             }
         }
     }
@@ -498,11 +510,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     p[e] = pack2<T>(s[x], s[x + 1]);
                 }
                 tmem_st_32x32b_x16(s_addr + c * 16, p);
-                if (c & 1) {  // half of the keys: their product may begin
+                if (c % (4 / kParts) == 4 / kParts - 1) {  // a part of the keys: its product may begin
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars.p[i][c >> 1]));
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.p[i][c / (4 / kParts)]));
                 }
             }
             // the row's sum, of the unrounded weights, while the product runs
