@@ -69,11 +69,18 @@ struct TcArgs {
     int *status;
 };
 
-// What a CTA works on: query tokens [t0, t0 + tokens) of the sequence's lq (row q0 first), its
-// keys [k0, k0 + lk).
+// One piece of work: kv head hk, the query tokens from t0 on of a sequence of lq (row q0 first)
+// with lk keys (row k0 first), and which of the key splits.
 struct Item {
-    int q0, lq, k0, lk, t0;
+    int q0, lq, k0, lk, t0, hk, split;
     int valid;
+    int odd;  // set while it is worked on: a non-finite value was taken out of a V tile
+};
+
+// Its key tiles: [ja, jb[i]) for half i, jb for both; vis_lo: the keys that all of its rows see.
+struct Range {
+    int ja, jb0, jb1, jb, vis_lo;
+    bool two_halves;
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -132,39 +139,95 @@ __device__ __forceinline__ void seq_bounds(const int32_t *cu, int64_t s, int64_t
     len = int(max(b - a, int64_t(0)));
 }
 
-// The tile'th tile of `span` tokens, counted over the sequences in order.  One warp.
-__device__ __forceinline__ void find_item(const TcArgs &a, int64_t tile, int span, int lane, Item &it) {
-    it.valid = 0;
-    if (!a.cu_q) {
-        it = {0, int(a.tokens_q), 0, int(a.tokens_k), int(tile * span), tile * span < a.tokens_q};
-        return;
+// One sequence's query tiles of `span` tokens.
+struct Tiles {
+    int q0, lq, lk, count;
+
+    // The first of its tiles whose last token sees keys of at least x key tiles, `count` if there is
+    // none; the tiles after it see at least as many.
+    __device__ __forceinline__ int first_with(int x, int span, int causal) const {
+        const int64_t keys = int64_t(kKeys) * (x - 1) + 1;
+        if (x <= 0) return 0;
+        if (lk < keys) return count;
+        if (!causal) return 0;
+        return int(max((keys - lk + lq + span - 1) / span - 1, int64_t(0)));
     }
-    int64_t before = 0;
-    for (int64_t s0 = 0; s0 < a.n_seqs; s0 += 32) {
-        const int64_t s = s0 + lane;
-        int q0 = 0, lq = 0;
-        if (s < a.n_seqs) seq_bounds(a.cu_q, s, a.tokens_q, q0, lq);
-        const int64_t tiles = (int64_t(lq) + span - 1) / span;
-        int64_t incl = tiles;
+};
+
+__device__ __forceinline__ Tiles tiles_of(const TcArgs &a, int64_t s, int span) {
+    Tiles t = {0, 0, 0, 0};
+    if (s < a.n_seqs) {
+        int k0;
+        seq_bounds(a.cu_q, s, a.tokens_q, t.q0, t.lq);
+        seq_bounds(a.cu_k, s, a.tokens_k, k0, t.lk);
+        t.count = int((int64_t(t.lq) + span - 1) / span);
+    }
+    return t;
+}
+
+// The rank'th tile of `span` tokens, most key tiles first (so that the last items to start are
+// short ones), or for many sequences, where that search would take longer than it saves, the
+// last sequence's last tile first.  One warp; false when there is no such tile.
+constexpr int kSortedSeqs = 32;
+__device__ __forceinline__ bool find_item(const TcArgs &a, int64_t rank, int span, int lane, Item &it) {
+    if (!a.cu_q) {
+        it.q0 = it.k0 = 0;
+        it.lq = int(a.tokens_q);
+        it.lk = int(a.tokens_k);
+        it.t0 = int(rank * span);
+        return rank * span < a.tokens_q;
+    }
+    if (a.n_seqs <= kSortedSeqs) {
+        const Tiles t = tiles_of(a, lane, span);
+        if (rank >= __reduce_add_sync(0xffffffffu, unsigned(t.count))) return false;
+        // the largest x for which more than `rank` tiles see at least x key tiles
+        int lo = 0, hi = int(__reduce_max_sync(0xffffffffu, unsigned(t.lk)) / kKeys) + 2;
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            const unsigned n = __reduce_add_sync(0xffffffffu, unsigned(t.count - t.first_with(mid, span, a.causal)));
+            if (n > rank) lo = mid;
+            else hi = mid;
+        }
+        const int first = t.first_with(lo, span, a.causal), next = t.first_with(hi, span, a.causal);
+        // rank among the tiles with exactly lo key tiles, sequence by sequence
+        const unsigned left = unsigned(rank) - __reduce_add_sync(0xffffffffu, unsigned(t.count - next));
+        unsigned incl = unsigned(next - first);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+            const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += x;
         }
-        const int64_t first = before + incl - tiles;
-        const unsigned hit = __ballot_sync(0xffffffffu, tile >= first && tile < first + tiles);
+        const unsigned before = incl - unsigned(next - first);
+        const int src = __ffs(__ballot_sync(0xffffffffu, left >= before && left < incl)) - 1;
+        it.q0 = __shfl_sync(0xffffffffu, t.q0, src);
+        it.lq = __shfl_sync(0xffffffffu, t.lq, src);
+        it.t0 = int(__shfl_sync(0xffffffffu, unsigned(first) - before, src) + left) * span;
+        seq_bounds(a.cu_k, src, a.tokens_k, it.k0, it.lk);
+        return true;
+    }
+    int64_t before = 0;
+    for (int64_t s0 = (a.n_seqs - 1) / 32 * 32; s0 >= 0; s0 -= 32) {  // lane l: the l'th sequence from the chunk's end
+        const int64_t s = s0 + 31 - lane;
+        const Tiles t = tiles_of(a, s, span);
+        unsigned incl = unsigned(t.count);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const int64_t last = before + incl, first = last - t.count;
+        const unsigned hit = __ballot_sync(0xffffffffu, rank >= first && rank < last);
         if (hit) {
             const int src = __ffs(hit) - 1;
-            const int64_t ss = s0 + src;
-            it.q0 = __shfl_sync(0xffffffffu, q0, src);
-            it.lq = __shfl_sync(0xffffffffu, lq, src);
-            it.t0 = int((tile - __shfl_sync(0xffffffffu, first, src)) * span);
-            seq_bounds(a.cu_k, ss, a.tokens_k, it.k0, it.lk);
-            it.valid = 1;
-            return;
+            it.q0 = __shfl_sync(0xffffffffu, t.q0, src);
+            it.lq = __shfl_sync(0xffffffffu, t.lq, src);
+            it.t0 = int(__shfl_sync(0xffffffffu, int(last - 1 - rank), src)) * span;
+            seq_bounds(a.cu_k, s0 + 31 - src, a.tokens_k, it.k0, it.lk);
+            return true;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
     }
+    return false;
 }
 
 // Keys that query token t of the sequence sees.
@@ -172,6 +235,25 @@ __device__ __forceinline__ int visible(const TcArgs &a, const Item &it, int t) {
     if (!a.causal) return it.lk;
     const int64_t n = int64_t(t) + 1 + it.lk - it.lq;
     return int(min(max(n, int64_t(0)), int64_t(it.lk)));
+}
+
+__device__ __forceinline__ Range range_of(const TcArgs &a, const Item &it) {
+    Range r;
+    r.vis_lo = visible(a, it, it.t0);
+    r.two_halves = it.t0 + a.per_half < it.lq;
+    int n[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int first = it.t0 + i * a.per_half, last = min(first + a.per_half, it.lq) - 1;
+        n[i] = last >= first ? (visible(a, it, last) + kKeys - 1) / kKeys : 0;
+    }
+    const int most = max(n[0], n[1]), per_split = (most + a.splits - 1) / a.splits;
+    const int end = min((it.split + 1) * per_split, most);
+    r.ja = min(it.split * per_split, most);
+    r.jb0 = max(min(end, n[0]), r.ja);
+    r.jb1 = max(min(end, n[1]), r.ja);
+    r.jb = max(r.jb0, r.jb1);
+    return r;
 }
 
 template <typename T> struct Bits;
@@ -213,16 +295,44 @@ template <typename T, int DP> __device__ __forceinline__ bool clean_values(uint8
     return __any_sync(0xffffffffu, seen != 0);
 }
 
-// Stages are released in pairs, (V_j, K_{j+1}) after K_0 alone, by the softmax threads: a half's
-// scores S(j+1) are complete after its products on both.  No half gets as many as kReleases pairs
-// ahead of the other: the ring holds at most 5 pairs, and the halves' numbers of tiles differ by
-// at most 2.
-constexpr int kReleases = 16;
-constexpr int kParts = 2;  // parts of a tile's weights that are handed over one by one
+constexpr int kParts = 2;      // parts of a tile's weights that are handed over one by one
+constexpr int kItemRoles = 11;  // warps that read an item: softmax, copies, products, gate
 
 struct Bars {
-    uint64_t q, full[8], clean[8], empty[kReleases], s[2], p[2][2], o[2], drain;
+    uint64_t full[8], empty[8], clean[8];  // the ring's stages; empty and q_empty: one arrival a half
+    uint64_t q, q_empty;
+    uint64_t s[2], p[2][kParts], o[2];     // scores complete, weights stored, output complete
+    uint64_t item[2], item_empty[2], want, next, drain;
 };
+
+// Ask the hardware for the next block of the grid that has not started: its index, or -1.  One warp.
+__device__ __forceinline__ int64_t take_next_block(uint4 *answer, uint32_t bar, uint32_t parity, int lane,
+                                                   volatile int *abort) {
+    if (lane == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(bar, 16);
+        asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                         smem_u32(answer)),
+                     "r"(bar)
+                     : "memory");
+    }
+    __syncwarp();
+    if (!warp_wait(bar, parity, abort)) {
+        int never = 0;
+        warp_wait(bar, parity, &never);  // the answer lands before shared memory is released
+        return -1;
+    }
+    uint32_t yes, id;
+    asm volatile(
+        "{\n.reg .b128 r;\n.reg .pred p;\nld.shared.b128 r, [%2];\n"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}"
+        : "=r"(yes), "=r"(id)
+        : "r"(smem_u32(answer))
+        : "memory");
+    __syncwarp();
+    return yes ? int64_t(id) : -1;
+}
 
 template <typename T, int DP>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ TcArgs a) {
@@ -230,47 +340,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     constexpr int ST = P::kStages;
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
-    __shared__ Item item_s;
+    __shared__ Item items[2];
+    __shared__ __align__(16) uint4 answer;
     __shared__ uint32_t tmem_s;
-    __shared__ int abort_s, odd_values;
+    __shared__ int abort_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (blockIdx.x == 0 && tid == 0) *a.status = QMM_OK;
     grid_launch_dependents();  // a launch that waits for this one's end may take free SMs
 
-    // blocks in order: all heads and splits of a tile, the last tiles (most keys) first
-    int64_t rest = int64_t(gridDim.x) - 1 - blockIdx.x;
-    const int hk = int(rest % a.shape.hk);
-    rest /= a.shape.hk;
-    const int split = int(rest % a.splits);
-    const int64_t tile = rest / a.splits;
-
-    if (warp == 9) {
-        Item it;
-        find_item(a, tile, 2 * a.per_half, lane, it);
-        if (lane == 0) {
-            item_s = it;
-            abort_s = 0;
-            odd_values = 0;
-            mbar_init(smem_u32(&bars.q), 1);
-            for (int i = 0; i < ST; ++i) {
-                mbar_init(smem_u32(&bars.full[i]), 1);
-                mbar_init(smem_u32(&bars.clean[i]), 1);
-            }
-            const bool two_halves = it.t0 + a.per_half < it.lq;
-            for (int i = 0; i < kReleases; ++i) mbar_init(smem_u32(&bars.empty[i]), two_halves ? 2 : 1);
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(smem_u32(&bars.s[i]), 1);
-                mbar_init(smem_u32(&bars.p[i][0]), 5);
-                mbar_init(smem_u32(&bars.p[i][1]), 4);
-                mbar_init(smem_u32(&bars.o[i]), 1);
-            }
-            mbar_init(smem_u32(&bars.drain), 1);
-            fence_mbar_init();
+    if (tid == 0) {
+        abort_s = 0;
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(smem_u32(&bars.full[i]), 1);
+            mbar_init(smem_u32(&bars.empty[i]), 2);
+            mbar_init(smem_u32(&bars.clean[i]), 1);
         }
+        mbar_init(smem_u32(&bars.q), 1);
+        mbar_init(smem_u32(&bars.q_empty), 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&bars.s[i]), 1);
+            for (int h = 0; h < kParts; ++h) mbar_init(smem_u32(&bars.p[i][h]), h == 0 ? 5 : 4);
+            mbar_init(smem_u32(&bars.o[i]), 1);
+            mbar_init(smem_u32(&bars.item[i]), 1);
+            mbar_init(smem_u32(&bars.item_empty[i]), kItemRoles);
+        }
+        mbar_init(smem_u32(&bars.want), 1);
+        mbar_init(smem_u32(&bars.next), 1);
+        mbar_init(smem_u32(&bars.drain), 1);
+        fence_mbar_init();
     }
-    __syncthreads();
-    const Item it = item_s;
-    if (!it.valid) return;
     if (warp == 8) {
         tmem_alloc(smem_u32(&tmem_s), 512);
         tmem_relinquish();
@@ -284,119 +381,161 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     const uint32_t sm0 = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t sq = sm0, skv = sm0 + 2 * P::kTile;
 
-    // key tiles [ja, jb[i]) of each half; vis_lo: the keys that every row of the CTA sees
-    const int half_tokens = a.per_half;
-    const bool two_halves = it.t0 + half_tokens < it.lq;
-    const int vis_lo = visible(a, it, it.t0);
-    int n[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int first = it.t0 + i * half_tokens, last = min(first + half_tokens, it.lq) - 1;
-        n[i] = last >= first ? (visible(a, it, last) + kKeys - 1) / kKeys : 0;
-    }
-    const int n_all = max(n[0], n[1]), per_split = (n_all + a.splits - 1) / a.splits;
-    const int ja = min(split * per_split, n_all), je = min(ja + per_split, n_all);
-    const int jb0 = max(min(je, n[0]), ja), jb1 = max(min(je, n[1]), ja);
-    const int jb = max(jb0, jb1);
+    // The k'th item of this CTA, for a whole warp; false at the end.
+    auto get_item = [&](int k, Item &it) -> bool {
+        if (!warp_wait(smem_u32(&bars.item[k & 1]), (k >> 1) & 1, abort)) return false;
+        it = items[k & 1];
+        return it.valid;
+    };
+    auto done_with_item = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.item_empty[k & 1]));
+    };
+    // Parities: an item's first ring stage, tile of half i, ... is counted over all items of the CTA.
+    uint32_t base = 0, tiles0 = 0, tiles1 = 0, worked = 0;  // stages, tiles of each half, items with keys
+    auto advance = [&](const Range &r) {
+        base += 2 * (r.jb - r.ja);
+        tiles0 += r.jb0 - r.ja;
+        tiles1 += r.jb1 - r.ja;
+        worked += r.jb > r.ja;
+    };
 
     if (warp >= 8) {
     regs_dec<kOtherRegs>();
-    if (warp == 8) {
-        // ------------------------------------------------ copies
-        const int t_row = it.q0 + it.t0;
-        bool ok = true;
-        int issued = 0;
-        // After tile j's copy has arrived.  The tiles to clean lie within the 255 keys that the
-        // CTA's first and last row differ by, at most 3, so no stage is cleaned twice.
-        auto clean = [&](int j) {
-            if ((j + 1) * kKeys <= vis_lo) return;
-            const int item = 2 * (j - ja) + 1, stg = item % ST;
-            ok = warp_wait(smem_u32(&bars.full[stg]), (item / ST) & 1, abort);
-            if (!ok) return;
-            const bool odd = clean_values<T, DP>(raw + (sm0 - smem_u32(raw)) + (2 + stg) * P::kTile,
-                                                 max(vis_lo - j * kKeys, 0), min(it.lk - j * kKeys, kKeys), lane);
+    if (warp == 11) {
+        // ------------------------------------------------ items: this block's, then blocks that have not started
+        int64_t id = blockIdx.x;
+        int asked = 0;
+        for (int k = 0;; ++k) {
+            if (k >= 2 && !warp_wait(smem_u32(&bars.item_empty[k & 1]), ((k >> 1) - 1) & 1, abort)) break;
+            Item it;
+            it.valid = 0;
+            if (id >= 0) {
+                if (id == 0 && lane == 0) *a.status = QMM_OK;  // long before a wait can give up
+                // blocks in order: all heads and splits of a tile, then the next tile
+                int64_t rest = id;
+                it.hk = int(rest % a.shape.hk);
+                rest /= a.shape.hk;
+                it.split = int(rest % a.splits);
+                it.valid = find_item(a, rest / a.splits, 2 * a.per_half, lane, it);  // no tile: no later block has one
+            }
             if (lane == 0) {
-                if (odd) odd_values = 1;
-                mbar_arrive(smem_u32(&bars.clean[stg]));
+                it.odd = 0;
+                items[k & 1] = it;
+                mbar_arrive(smem_u32(&bars.item[k & 1]));
             }
             __syncwarp();
-        };
-        if (jb > ja && lane == 0) {
+            if (!it.valid) break;
+            // the next one once this one's copies are under way: not earlier, or the last items
+            // would wait behind long ones
+            if (!warp_wait(smem_u32(&bars.want), k & 1, abort)) break;
+            id = take_next_block(&answer, smem_u32(&bars.next), asked++ & 1, lane, abort);
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------ copies
+        bool ok = true;
+        uint32_t issued = 0;
+        if (lane == 0) {
             prefetch_tmap(&a.q);
             prefetch_tmap(&a.k);
             prefetch_tmap(&a.v);
-            const uint32_t bar = smem_u32(&bars.q), box = uint32_t(a.group * half_tokens) * 128;
-            const bool both = jb1 > ja, one = jb0 > ja;
-            mbar_arrive_expect_tx(bar, box * (DP / 64) * (uint32_t(one) + uint32_t(both)));
-            for (int i = 0; i < 2; ++i)
-                for (int b = 0; b < DP / 64; ++b)
-                    if (i ? both : one)
-                        tma_load_3d(sq + i * P::kTile + b * kRows * 128, &a.q, b * 64, hk * a.group,
-                                    t_row + i * half_tokens, bar);
         }
-        for (int j = ja; j < jb && ok; ++j) {
-            for (int kv = 0; kv < 2 && ok; ++kv) {
-                const int item = 2 * (j - ja) + kv, stg = item % ST;
-                if (item >= ST) {
-                    const int pair = (item - ST + 1) / 2;
-                    ok = warp_wait(smem_u32(&bars.empty[pair % kReleases]), (pair / kReleases) & 1, abort);
+        Item it;
+        for (int k = 0; get_item(k, it); ++k) {
+            const Range r = range_of(a, it);
+            auto clean = [&](int j) {  // after tile j's copy has arrived
+                if ((j + 1) * kKeys <= r.vis_lo) return;
+                const uint32_t n = base + 2 * (j - r.ja) + 1, stg = n % ST;
+                ok = warp_wait(smem_u32(&bars.full[stg]), (n / ST) & 1, abort);
+                if (!ok) return;
+                const bool odd = clean_values<T, DP>(raw + (sm0 - smem_u32(raw)) + (2 + stg) * P::kTile,
+                                                     max(r.vis_lo - j * kKeys, 0), min(it.lk - j * kKeys, kKeys), lane);
+                if (lane == 0) {
+                    if (odd) items[k & 1].odd = 1;
+                    mbar_arrive(smem_u32(&bars.clean[stg]));
                 }
+                __syncwarp();
+            };
+            if (r.jb > r.ja) {
+                if (worked > 0) ok = warp_wait(smem_u32(&bars.q_empty), (worked - 1) & 1, abort);
                 if (ok && lane == 0) {
-                    const uint32_t bar = smem_u32(&bars.full[stg]);
-                    mbar_arrive_expect_tx(bar, P::kTile);
-                    for (int b = 0; b < DP / 64; ++b)
-                        tma_load_3d(skv + stg * P::kTile + b * kKeys * 128, kv ? &a.v : &a.k, b * 64, hk,
-                                    it.k0 + j * kKeys, bar);
+                    const uint32_t bar = smem_u32(&bars.q), box = uint32_t(a.group * a.per_half) * 128;
+                    const bool half[2] = {r.jb0 > r.ja, r.jb1 > r.ja};
+                    mbar_arrive_expect_tx(bar, box * (DP / 64) * (uint32_t(half[0]) + uint32_t(half[1])));
+                    for (int i = 0; i < 2; ++i)
+                        for (int b = 0; b < DP / 64; ++b)
+                            if (half[i])
+                                tma_load_3d(sq + i * P::kTile + b * kRows * 128, &a.q, b * 64, it.hk * a.group,
+                                            it.q0 + it.t0 + i * a.per_half, bar);
                 }
-                if (ok) issued = item + 1;
                 __syncwarp();
             }
-            // a tile is cleaned once the next one's copies are under way
-            if (ok && j > ja) clean(j - 1);
+            for (int j = r.ja; j < r.jb && ok; ++j) {
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    const uint32_t n = base + 2 * (j - r.ja) + kv, stg = n % ST;
+                    if (n >= ST) ok = warp_wait(smem_u32(&bars.empty[stg]), (n / ST - 1) & 1, abort);
+                    if (ok && lane == 0) {
+                        const uint32_t bar = smem_u32(&bars.full[stg]);
+                        mbar_arrive_expect_tx(bar, P::kTile);
+                        for (int b = 0; b < DP / 64; ++b)
+                            tma_load_3d(skv + stg * P::kTile + b * kKeys * 128, kv ? &a.v : &a.k, b * 64, it.hk,
+                                        it.k0 + j * kKeys, bar);
+                    }
+                    if (ok) issued = n + 1;
+                    __syncwarp();
+                }
+                // a tile is cleaned once the next one's copies are under way
+                if (ok && j > r.ja) clean(j - 1);
+            }
+            if (lane == 0) mbar_arrive(smem_u32(&bars.want));
+            if (ok && r.jb > r.ja) clean(r.jb - 1);
+            advance(r);
+            if (!ok) break;
+            done_with_item(k);
         }
-        if (ok && jb > ja) clean(jb - 1);
-        if (!ok) {  // a wait gave up: the copies in flight land before shared memory is released
+        if (*abort) {  // a wait gave up: the copies in flight land before shared memory is released
             int never = 0;
-            warp_wait(smem_u32(&bars.q), 0, &never);
-            for (int item = max(issued - ST, 0); item < issued; ++item) {
+            if (worked > 0) warp_wait(smem_u32(&bars.q), (worked - 1) & 1, &never);
+            for (uint32_t n = issued > ST ? issued - ST : 0; n < issued; ++n) {
                 never = 0;
-                warp_wait(smem_u32(&bars.full[item % ST]), (item / ST) & 1, &never);
+                warp_wait(smem_u32(&bars.full[n % ST]), (n / ST) & 1, &never);
             }
         }
     } else if (warp == 9) {
         // ------------------------------------------------ products, issued by one elected lane
-        if (jb > ja) {
-            bool ok = spin_wait(smem_u32(&bars.q), 0, abort);
-            auto full = [&](int item) {
-                ok = ok && spin_wait(smem_u32(&bars.full[item % ST]), (item / ST) & 1, abort);
-            };
-            const uint64_t qd = smem_desc(sq, 1024, 2);
-            auto qk = [&](int i, int item) {
-                const uint64_t kd = smem_desc(skv + uint32_t(item % ST) * P::kTile, 1024, 2);
-                if (elect_one()) {
+        bool ok = true;
+        const uint64_t qd = smem_desc(sq, 1024, 2), kd0 = smem_desc(skv, 1024, 2), vd0 = smem_desc_mn(skv, kKeys * 128);
+        auto qk = [&](int i, uint32_t n) {
+            const uint64_t kd = kd0 + uint32_t((n % ST) * P::kTile >> 4);
+            if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < DP / 16; ++s) {
-                        const uint32_t off = (uint32_t(s / 4) * kRows * 128 + uint32_t(s % 4) * 32) >> 4;
-                        mma_f16(tmem + i * kKeys, qd + uint32_t(i * P::kTile >> 4) + off, kd + off, a.idesc_qk, s != 0);
-                    }
-                    mma_commit(smem_u32(&bars.s[i]));
+                for (int s = 0; s < DP / 16; ++s) {
+                    const uint32_t off = (uint32_t(s / 4) * kRows * 128 + uint32_t(s % 4) * 32) >> 4;
+                    mma_f16(tmem + i * kKeys, qd + uint32_t(i * P::kTile >> 4) + off, kd + off, a.idesc_qk, s != 0);
                 }
-                __syncwarp();
-            };
-            full(0);
-            tc_fence_after();
-            if (ok && jb0 > ja) qk(0, 0);
-            if (ok && jb1 > ja) qk(1, 0);
-            const uint64_t vd0 = smem_desc_mn(skv, kKeys * 128);
+                mma_commit(smem_u32(&bars.s[i]));
+            }
+            __syncwarp();
+        };
+        Item it;
+        for (int k = 0; ok && get_item(k, it); ++k) {
+            const Range r = range_of(a, it);
+            if (r.jb > r.ja) {
+                ok = spin_wait(smem_u32(&bars.q), worked & 1, abort) &&
+                     spin_wait(smem_u32(&bars.full[base % ST]), (base / ST) & 1, abort);
+                tc_fence_after();
+                if (ok && r.jb0 > r.ja) qk(0, base);
+                if (ok && r.jb1 > r.ja) qk(1, base);
+            }
 #pragma unroll 1
-            for (int turn = 0; ok && turn < 2 * (jb - ja); ++turn) {
-                const int i = turn & 1, j = turn >> 1, left = (i ? jb1 : jb0) - ja - j;
+            for (int turn = 0; ok && turn < 2 * (r.jb - r.ja); ++turn) {
+                const int i = turn & 1, j = turn >> 1, left = (i ? r.jb1 : r.jb0) - r.ja - j;
                 if (left <= 0) continue;
-                const int vi = 2 * j + 1;
-                const uint64_t vd = vd0 + uint32_t((vi % ST) * P::kTile >> 4);
+                const uint32_t n = base + 2 * j + 1, tile = (i ? tiles1 : tiles0) + j;
+                const uint64_t vd = vd0 + uint32_t((n % ST) * P::kTile >> 4);
 #pragma unroll
                 for (int h = 0; h < kParts; ++h) {
-                    ok = ok && spin_wait(smem_u32(&bars.p[i][h]), j & 1, abort);
+                    ok = ok && spin_wait(smem_u32(&bars.p[i][h]), tile & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
@@ -408,181 +547,236 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (left > 1) qk(i, vi + 1);
+                if (left > 1) qk(i, n + 1);
                 else if (elect_one()) mma_commit(smem_u32(&bars.o[i]));
                 __syncwarp();
             }
-            if (!ok) {  // let what was issued end before the tensor memory is freed
-                if (elect_one()) mma_commit(smem_u32(&bars.drain));
-                int never = 0;
-                spin_wait(smem_u32(&bars.drain), 0, &never);
-            }
+            advance(r);
+            if (ok) done_with_item(k);
         }
-    } else if (warp == 10 && lane == 0) {
-        // ------------------------------------------------ gate: V_j and K_{j+1} have arrived
-        // One arrival of each half's P barrier, so that the issuer waits for nothing else.
+        if (*abort) {  // let what was issued end before the tensor memory is freed
+            if (elect_one()) mma_commit(smem_u32(&bars.drain));
+            int never = 0;
+            spin_wait(smem_u32(&bars.drain), 0, &never);
+        }
+    } else {
+        // ------------------------------------------------ gate (warp 10): V_j and K_{j+1} have arrived
+        // One arrival of each half's weight barrier, so that the issuer waits for nothing else, and
+        // the releases of a half that does not take part.
         bool ok = true;
-        for (int j = ja; j < jb && ok; ++j) {
-            const int vi = 2 * (j - ja) + 1;
-            ok = mbar_wait(smem_u32(&bars.full[vi % ST]), (vi / ST) & 1, abort);
-            if (ok && (j + 1) * kKeys > vis_lo) ok = mbar_wait(smem_u32(&bars.clean[vi % ST]), 0, abort);
-            if (ok && j + 1 < jb)
-                ok = mbar_wait(smem_u32(&bars.full[(vi + 1) % ST]), ((vi + 1) / ST) & 1, abort);
-            for (int i = 0; i < 2 && ok; ++i) {
-                if (j >= (i ? jb1 : jb0)) continue;
-                if (j > ja) ok = mbar_wait(smem_u32(&bars.p[i][0]), (j - ja - 1) & 1, abort);
-                if (ok) mbar_arrive(smem_u32(&bars.p[i][0]));
+        uint32_t cleans = 0;  // the parity of each stage's clean barrier
+        Item it;
+        for (int k = 0; ok && get_item(k, it); ++k) {
+            const Range r = range_of(a, it);
+            auto arrived = [&](uint32_t n) {
+                ok = ok && warp_wait(smem_u32(&bars.full[n % ST]), (n / ST) & 1, abort);
+            };
+            if (r.jb > r.ja) {
+                arrived(base);
+                if (r.jb0 == r.ja || r.jb1 == r.ja) {
+                    ok = ok && warp_wait(smem_u32(&bars.q), worked & 1, abort);
+                    if (ok && lane == 0) mbar_arrive(smem_u32(&bars.q_empty));
+                }
             }
+            for (int j = r.ja; j < r.jb && ok; ++j) {
+                const uint32_t n = base + 2 * (j - r.ja) + 1, stg = n % ST;
+                arrived(n);
+                if (ok && (j + 1) * kKeys > r.vis_lo) {
+                    ok = warp_wait(smem_u32(&bars.clean[stg]), (cleans >> stg) & 1, abort);
+                    cleans ^= 1u << stg;
+                }
+                if (j + 1 < r.jb) arrived(n + 1);
+                for (int i = 0; i < 2 && ok; ++i) {
+                    if (j >= (i ? r.jb1 : r.jb0)) {
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&bars.empty[(n - 1) % ST]));
+                            mbar_arrive(smem_u32(&bars.empty[stg]));
+                        }
+                        continue;
+                    }
+                    const uint32_t tile = (i ? tiles1 : tiles0) + (j - r.ja);
+                    if (tile > 0) ok = warp_wait(smem_u32(&bars.p[i][0]), (tile - 1) & 1, abort);
+                    if (ok && lane == 0) mbar_arrive(smem_u32(&bars.p[i][0]));
+                }
+                __syncwarp();
+            }
+            advance(r);
+            if (ok) done_with_item(k);
         }
     }
     } else {
         // ------------------------------------------------ softmax, one row a thread
         regs_inc<kSoftmaxRegs>();
-        const int i = warp >> 2, r = tid & 127, end = i ? jb1 : jb0;
+        // Little is kept over the tile loop next to the 128 scores: what the output needs of the
+        // item is read again (a spilled register costs hundreds of cycles: shared memory leaves
+        // next to no L1 cache).
+        const int i = warp >> 2;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 256 + i * DP;
-        const int t = it.t0 + i * half_tokens + r / a.group;
-        const bool row_valid = r < half_tokens * a.group && t < it.lq;
-        const int vis = row_valid ? visible(a, it, t) : 0;
-        // the keys that every row of this half sees
-        const int vis_half = visible(a, it, it.t0 + i * half_tokens);
-        float top = -INFINITY, sum0 = 0.f, sum1 = 0.f;
+        const bool releases = (tid & 127) == 0;
+        uint32_t tiles = 0, outputs = 0;  // tiles of this half so far, items in which it took part
         bool ok = true;
-        for (int j = ja; j < end; ++j) {
-            ok = warp_wait(smem_u32(&bars.s[i]), (j - ja) & 1, abort);
-            if (!ok) break;
-            if ((tid & 127) == 0) mbar_arrive(smem_u32(&bars.empty[(j - ja) % kReleases]));
-            tc_fence_after();
-            float s[kKeys];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + c * 32, *reinterpret_cast<float(*)[32]>(s + c * 32));
-            tmem_ld_wait();
-            loaded(s);
-            if ((j + 1) * kKeys > vis_half) {
-                const int left = vis - j * kKeys;
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c)
-                    if (c >= left) s[c] = -INFINITY;
+        for (int k = 0; ok; ++k) {
+            ok = warp_wait(smem_u32(&bars.item[k & 1]), (k >> 1) & 1, abort);
+            if (!ok || !items[k & 1].valid) break;
+            // tiles to do and to count for the ring; keys from the first tile on that this row,
+            // and that every row of the half, sees
+            int count, stages, vis, vis_half;
+            {
+                const Item it = items[k & 1];
+                const Range r = range_of(a, it);
+                count = (i ? r.jb1 : r.jb0) - r.ja;
+                stages = 2 * (r.jb - r.ja);
+                const int first = it.t0 + i * a.per_half, mine = (tid & 127) / a.group, t = first + mine;
+                vis = (mine < a.per_half && t < it.lq ? visible(a, it, t) : 0) - r.ja * kKeys;
+                vis_half = visible(a, it, first) - r.ja * kKeys;
             }
-            float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+            float top = -INFINITY, sum0 = 0.f, sum1 = 0.f;
+#pragma unroll 1
+            for (int j = 0; j < count; ++j) {
+                ok = warp_wait(smem_u32(&bars.s[i]), (tiles + j) & 1, abort);
+                if (!ok) break;
+                if (releases) {  // S_i(j) is complete: so are O_i's product with V_{j-1} and the reads of K_j
+                    const uint32_t n = base + 2 * j;
+                    mbar_arrive(smem_u32(&bars.empty[n % ST]));
+                    if (j > 0) mbar_arrive(smem_u32(&bars.empty[(n - 1) % ST]));
+                    if (j + 1 == count) mbar_arrive(smem_u32(&bars.q_empty));
+                }
+                tc_fence_after();
+                float s[kKeys];
 #pragma unroll
-            for (int c = 4; c < kKeys; c += 8) {
-                m0 = max3(m0, s[c], s[c + 1]);
-                m1 = max3(m1, s[c + 2], s[c + 3]);
-                if (c + 4 < kKeys) {
-                    m2 = max3(m2, s[c + 4], s[c + 5]);
-                    m3 = max3(m3, s[c + 6], s[c + 7]);
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + c * 32, *reinterpret_cast<float(*)[32]>(s + c * 32));
+                tmem_ld_wait();
+                loaded(s);
+                if ((j + 1) * kKeys > vis_half) {
+                    const int left = vis - j * kKeys;
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c)
+                        if (c >= left) s[c] = -INFINITY;
+                }
+                float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+                for (int c = 4; c < kKeys; c += 8) {
+                    m0 = max3(m0, s[c], s[c + 1]);
+                    m1 = max3(m1, s[c + 2], s[c + 3]);
+                    if (c + 4 < kKeys) {
+                        m2 = max3(m2, s[c + 4], s[c + 5]);
+                        m3 = max3(m3, s[c + 6], s[c + 7]);
+                    }
+                }
+                const float most = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                // move the maximum when a score passes it by more than the slack
+                const bool move = (most - top) * a.scale_log2 > kSlack || (top == -INFINITY && most > -INFINITY);
+                if (j == 0) {
+                    if (move) top = most;
+                } else if (__any_sync(0xffffffffu, move)) {
+                    const float now = move ? most : top;
+                    const float f = top == -INFINITY ? 1.f : ex2((top - now) * a.scale_log2);
+                    top = now;
+                    sum0 *= f;
+                    sum1 *= f;
+                    // S_i(j) was issued after O_i's last product, so that one is done
+#pragma unroll
+                    for (int c = 0; c < DP / 16; ++c) {
+                        float o[16];
+                        tmem_ld_32x32b_x16(o_addr + c * 16, o);
+                        tmem_ld_wait();
+                        loaded(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= f;
+                        tmem_st_32x32b_x16(o_addr + c * 16, o);
+                    }
+                }
+                const float shift = top == -INFINITY ? 0.f : -top * a.scale_log2;
+#pragma unroll
+                for (int c = 0; c < kKeys / 32; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int x = c * 32 + 2 * e;
+                        fma2(s[x], s[x + 1], s[x], s[x + 1], a.scale_log2, shift);
+                        s[x] = ex2(s[x]);
+                        s[x + 1] = ex2(s[x + 1]);
+                        p[e] = pack2<T>(s[x], s[x + 1]);
+                        add2(sum0, sum1, s[x], s[x + 1]);
+                    }
+                    tmem_st_32x32b_x16(s_addr + c * 16, p);
+                    if (c % (4 / kParts) == 4 / kParts - 1) {  // a part of the keys: its product may begin
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bars.p[i][c / (4 / kParts)]));
+                    }
                 }
             }
-            const float most = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-            // move the maximum when a score passes it by more than the slack
-            const bool move = (most - top) * a.scale_log2 > kSlack || (top == -INFINITY && most > -INFINITY);
-            if (j == ja) {
-                if (move) top = most;
-            } else if (__any_sync(0xffffffffu, move)) {
-                const float base = move ? most : top;
-                const float f = top == -INFINITY ? 1.f : ex2((top - base) * a.scale_log2);
-                top = base;
-                sum0 *= f;
-                sum1 *= f;
-                // S_i(j) was issued after O_i's last product, so that one is done
+            if (ok && count > 0) {
+                ok = warp_wait(smem_u32(&bars.o[i]), outputs & 1, abort);
+                ++outputs;
+                if (ok && releases) mbar_arrive(smem_u32(&bars.empty[(base + 2 * count - 1) % ST]));
+            }
+            if (ok) {
+                tc_fence_after();
+                const Item it = items[k & 1];
+                const int mine = (tid & 127) / a.group, t = it.t0 + i * a.per_half + mine;
+                const bool row_valid = mine < a.per_half && t < it.lq;
+                const float sum = count > 0 ? sum0 + sum1 : 0.f;
+                const bool none = !(sum != 0.f);  // no key seen (a NaN sum is not none)
+                const float inv = none ? 0.f : 1.f / sum;
+                const int head = it.hk * a.group + (tid & 127) - mine * a.group;
+                const int64_t row = (int64_t(it.q0) + t) * a.shape.hq + head;
+                const bool odd = count > 0 && it.odd;
 #pragma unroll
                 for (int c = 0; c < DP / 32; ++c) {
                     float o[32];
-                    tmem_ld_32x32b_x32(o_addr + c * 32, o);
-                    tmem_ld_wait();
-                    loaded(o);
+                    if (count > 0) {
+                        tmem_ld_32x32b_x32(o_addr + c * 32, o);
+                        tmem_ld_wait();
+                        loaded(o);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= f;
-                    tmem_st_32x32b_x32(o_addr + c * 32, o);
-                }
-            }
-            const float shift = top == -INFINITY ? 0.f : -top * a.scale_log2;
+                    for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                    if (!row_valid || c * 32 >= a.shape.d) continue;
+                    if (odd) {
+                        const Range r = range_of(a, it);
+                        const int odd_from = max(r.vis_lo, r.ja * kKeys);
+                        const int odd_to = min(visible(a, it, t), (r.ja + count) * kKeys);
+                        const T *v = static_cast<const T *>(a.v_data) + it.hk * a.sv.h + c * 32;
+                        for (int key = odd_from; key < odd_to; ++key) {
+                            const T *vr = v + (int64_t(it.k0) + key) * a.sv.t;
 #pragma unroll
-            for (int c = 0; c < kKeys / 32; ++c) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int x = c * 32 + 2 * e;
-                    fma2(s[x], s[x + 1], s[x], s[x + 1], a.scale_log2, shift);
-                    s[x] = ex2(s[x]);
-                    s[x + 1] = ex2(s[x + 1]);
-                    p[e] = pack2<T>(s[x], s[x + 1]);
-                }
-                tmem_st_32x32b_x16(s_addr + c * 16, p);
-                if (c % (4 / kParts) == 4 / kParts - 1) {  // a part of the keys: its product may begin
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&bars.p[i][c / (4 / kParts)]));
-                }
-            }
-            // the row's sum, of the unrounded weights, while the product runs
-            float a0 = s[0], a1 = s[1], b0 = s[2], b1 = s[3];
-#pragma unroll
-            for (int c = 4; c < kKeys; c += 4) {
-                add2(a0, a1, s[c], s[c + 1]);
-                add2(b0, b1, s[c + 2], s[c + 3]);
-            }
-            add2(a0, a1, b0, b1);
-            add2(sum0, sum1, a0, a1);
-        }
-        if ((tid & 127) == 0 && (i == 0 || two_halves))  // tiles that only the other half takes
-            for (int j = end; j < jb; ++j) mbar_arrive(smem_u32(&bars.empty[(j - ja) % kReleases]));
-        if (ok && end > ja) ok = warp_wait(smem_u32(&bars.o[i]), 0, abort);
-        if (ok) {
-            tc_fence_after();
-            const float sum = end > ja ? sum0 + sum1 : 0.f;
-            const bool none = !(sum != 0.f);  // no key seen (a NaN sum is not none)
-            const float inv = none ? 0.f : 1.f / sum;
-            const int head = hk * a.group + r % a.group;
-            const int64_t row = (int64_t(it.q0) + t) * a.shape.hq + head;
-            const bool odd = end > ja && *(volatile int *)&odd_values;
-            const int odd_from = max(vis_lo, ja * kKeys), odd_to = min(vis, end * kKeys);
-#pragma unroll
-            for (int c = 0; c < DP / 32; ++c) {
-                float o[32];
-                if (end > ja) {
-                    tmem_ld_32x32b_x32(o_addr + c * 32, o);
-                    tmem_ld_wait();
-                    loaded(o);
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
-                if (!row_valid || c * 32 >= a.shape.d) continue;
-                if (odd) {
-                    const T *v = static_cast<const T *>(a.v_data) + hk * a.sv.h + c * 32;
-                    for (int key = odd_from; key < odd_to; ++key) {
-                        const T *vr = v + (int64_t(it.k0) + key) * a.sv.t;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (c * 32 + e >= a.shape.d) continue;
-                            const float x = float(vr[e]);
-                            if (!isfinite(x)) o[e] += x;
+                            for (int e = 0; e < 32; ++e) {
+                                if (c * 32 + e >= a.shape.d) continue;
+                                const float x = float(vr[e]);
+                                if (!isfinite(x)) o[e] += x;
+                            }
                         }
                     }
+                    if (!a.part) {
+                        T *dst = static_cast<T *>(a.out) + (int64_t(it.q0) + t) * a.so.t + head * a.so.h + c * 32;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            if (c * 32 + e < a.shape.d)
+                                *reinterpret_cast<uint4 *>(dst + e) =
+                                    make_uint4(pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
+                                               pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
+                    } else {
+                        float *dst = a.part + (int64_t(it.split) * a.tokens_q * a.shape.hq + row) * a.shape.d + c * 32;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            if (c * 32 + e < a.shape.d)
+                                *reinterpret_cast<float4 *>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
                 }
-                if (!a.part) {
-                    T *dst = static_cast<T *>(a.out) + (int64_t(it.q0) + t) * a.so.t + head * a.so.h + c * 32;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        if (c * 32 + e < a.shape.d)
-                            *reinterpret_cast<uint4 *>(dst + e) =
-                                make_uint4(pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
-                                           pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
-                } else {
-                    float *dst = a.part + (int64_t(split) * a.tokens_q * a.shape.hq + row) * a.shape.d + c * 32;
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        if (c * 32 + e < a.shape.d)
-                            *reinterpret_cast<float4 *>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                if (row_valid) {
+                    const float l2 = none ? -INFINITY : top * a.scale_log2 + log2f(sum);
+                    if (a.part) a.part_lse[int64_t(it.split) * a.tokens_q * a.shape.hq + row] = l2;
+                    else if (a.lse) a.lse[row] = l2 * kLn2;
                 }
             }
-            if (row_valid) {
-                const float l2 = none ? -INFINITY : top * a.scale_log2 + log2f(sum);
-                if (a.part) a.part_lse[int64_t(split) * a.tokens_q * a.shape.hq + row] = l2;
-                else if (a.lse) a.lse[row] = l2 * kLn2;
-            }
+            tc_fence_before();
+            base += stages;
+            tiles += count;
+            if (ok) done_with_item(k);
         }
     }
     tc_fence_before();
