@@ -43,12 +43,13 @@ constexpr int kTcThreads = 384;  // 168 registers each at launch: 64512 in all
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;  // 256 * 224 + 128 * 56 = 64512
 constexpr float kSlack = 8.0f;  // how far (in powers of two) a row's scores may pass its maximum
 
-// Shared-memory plan for a padded head size DP: Q_0, Q_1, then a ring of K and V tiles.  A tile
-// is DP/64 blocks of 128 rows x 128 bytes, 128-byte swizzled.
+// Shared-memory plan for a padded head size DP: Q_0, Q_1, a ring of K and V tiles, and 4 KB a
+// softmax warp for its output rows.  A tile is DP/64 blocks of 128 rows x 128 bytes, 128-byte swizzled.
 template <int DP> struct Plan {
     static constexpr int kTile = kRows * DP * 2;
-    static constexpr int kStages = DP == 128 ? 5 : 8;
-    static constexpr size_t kBytes = size_t(2 + kStages) * kTile + 1024;
+    static constexpr int kStages = DP == 128 ? 4 : 8;
+    static constexpr int kOut = (2 + kStages) * kTile;
+    static constexpr size_t kBytes = size_t(kOut) + 8 * 4096 + 1024;
 };
 
 struct TcArgs {
@@ -75,12 +76,9 @@ struct Item {
     int q0, lq, k0, lk, t0, hk, split;
     int valid;
     int odd;  // set while it is worked on: a non-finite value was taken out of a V tile
-};
-
-// Its key tiles: [ja, jb[i]) for half i, jb for both; vis_lo: the keys that all of its rows see.
-struct Range {
-    int ja, jb0, jb1, jb, vis_lo;
-    bool two_halves;
+    // its key tiles, [ja, jb0) and [ja, jb1) for the halves, [ja, jb) for either; the keys that all
+    // of its rows, and all rows of the second half, see
+    int ja, jb0, jb1, jb, vis_lo, vis_lo1;
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -237,69 +235,88 @@ __device__ __forceinline__ int visible(const TcArgs &a, const Item &it, int t) {
     return int(min(max(n, int64_t(0)), int64_t(it.lk)));
 }
 
-__device__ __forceinline__ Range range_of(const TcArgs &a, const Item &it) {
-    Range r;
-    r.vis_lo = visible(a, it, it.t0);
-    r.two_halves = it.t0 + a.per_half < it.lq;
+__device__ __forceinline__ void set_range(const TcArgs &a, Item &it) {
+    it.vis_lo = visible(a, it, it.t0);
+    it.vis_lo1 = visible(a, it, it.t0 + a.per_half);
     int n[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int first = it.t0 + i * a.per_half, last = min(first + a.per_half, it.lq) - 1;
         n[i] = last >= first ? (visible(a, it, last) + kKeys - 1) / kKeys : 0;
     }
-    const int most = max(n[0], n[1]), per_split = (most + a.splits - 1) / a.splits;
+    const int most = max(n[0], n[1]), per_split = a.splits > 1 ? (most + a.splits - 1) / a.splits : most;
     const int end = min((it.split + 1) * per_split, most);
-    r.ja = min(it.split * per_split, most);
-    r.jb0 = max(min(end, n[0]), r.ja);
-    r.jb1 = max(min(end, n[1]), r.ja);
-    r.jb = max(r.jb0, r.jb1);
-    return r;
+    it.ja = min(it.split * per_split, most);
+    it.jb0 = max(min(end, n[0]), it.ja);
+    it.jb1 = max(min(end, n[1]), it.ja);
+    it.jb = max(it.jb0, it.jb1);
 }
 
-template <typename T> struct Bits;
-template <> struct Bits<__half> {
+template <typename T> struct Pair;
+template <> struct Pair<__half> {
+    using type = __half2;
     static constexpr uint32_t kExp = 0x7c007c00u, kOne = 0x04000400u;
 };
-template <> struct Bits<__nv_bfloat16> {
+template <> struct Pair<__nv_bfloat16> {
+    using type = __nv_bfloat162;
     static constexpr uint32_t kExp = 0x7f807f80u, kOne = 0x00800080u;
 };
-// Nonzero (bits 15 and 31) where one of the two packed values is infinite or NaN.
-template <typename T> __device__ __forceinline__ uint32_t nonfinite2(uint32_t u) {
-    return ((u & Bits<T>::kExp) + Bits<T>::kOne) & 0x80008000u;
+// acc + 0 * u: stays zero until an infinity or NaN comes by, and is NaN from then on.
+template <typename T> __device__ __forceinline__ void taint(uint32_t &acc, uint32_t u) {
+    using P = typename Pair<T>::type;
+    const uint32_t zero = 0;
+    const P r = __hfma2(*reinterpret_cast<const P *>(&u), *reinterpret_cast<const P *>(&zero),
+                        *reinterpret_cast<const P *>(&acc));
+    acc = *reinterpret_cast<const uint32_t *>(&r);
+}
+// The packed pair without its infinite and NaN values.
+template <typename T> __device__ __forceinline__ uint32_t finite2(uint32_t u) {
+    const uint32_t bad = (u & Pair<T>::kExp) + Pair<T>::kOne;  // bits 15 and 31: exponent all ones
+    if (bad & 0x8000u) u &= 0xffff0000u;
+    if (bad & 0x80000000u) u &= 0x0000ffffu;
+    return u;
 }
 
 // A tile's V rows [from, end) may be unseen by some rows, and the rows from `end` on belong to
 // nobody: a weight of zero times what they hold must stay zero.  Rows from `end` on become
 // zeros; an infinity or NaN before `end` becomes zero and is reported (the rows that see it
-// take it in at the end).  One warp, on a tile of DP/64 blocks of 128 x 128 bytes.
+// take it in at the end).  One warp, on a tile of DP/64 blocks of 128 x 128 bytes; eight loads
+// in flight and one instruction a pair, or the tile's product would wait for this.
 template <typename T, int DP> __device__ __forceinline__ bool clean_values(uint8_t *tile, int from, int end, int lane) {
-    uint32_t seen = 0;
+    uint32_t acc[4] = {0, 0, 0, 0};
     for (int b = 0; b < DP / 64; ++b) {
         uint4 *rows = reinterpret_cast<uint4 *>(tile + b * kKeys * 128);
-        for (int i = from * 8 + lane; i < end * 8; i += 32) {
-            const uint4 u = rows[i];
-            const uint32_t x = nonfinite2<T>(u.x), y = nonfinite2<T>(u.y), z = nonfinite2<T>(u.z), w = nonfinite2<T>(u.w);
-            if (x | y | z | w) {
-                auto keep = [](uint32_t v, uint32_t bad) {
-                    if (bad & 0x8000u) v &= 0xffff0000u;
-                    if (bad & 0x80000000u) v &= 0x0000ffffu;
-                    return v;
-                };
-                rows[i] = make_uint4(keep(u.x, x), keep(u.y, y), keep(u.z, z), keep(u.w, w));
-                seen = 1;
+        for (int i0 = from * 8 + lane; i0 < end * 8; i0 += 32 * 8) {
+            uint4 u[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = rows[min(i0 + 32 * e, end * 8 - 1)];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                taint<T>(acc[0], u[e].x);
+                taint<T>(acc[1], u[e].y);
+                taint<T>(acc[2], u[e].z);
+                taint<T>(acc[3], u[e].w);
             }
         }
         for (int i = end * 8 + lane; i < kKeys * 8; i += 32) rows[i] = make_uint4(0, 0, 0, 0);
     }
+    const bool odd = __any_sync(0xffffffffu, (acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu);
+    if (odd) {
+        for (int b = 0; b < DP / 64; ++b) {
+            uint32_t *rows = reinterpret_cast<uint32_t *>(tile + b * kKeys * 128);
+#pragma unroll 1
+            for (int i = from * 32 + lane; i < end * 32; i += 32) rows[i] = finite2<T>(rows[i]);
+        }
+    }
     fence_proxy_async_smem();
-    return __any_sync(0xffffffffu, seen != 0);
+    return odd;
 }
 
 constexpr int kParts = 2;      // parts of a tile's weights that are handed over one by one
 constexpr int kItemRoles = 11;  // warps that read an item: softmax, copies, products, gate
 
 struct Bars {
-    uint64_t full[8], empty[8], clean[8];  // the ring's stages; empty and q_empty: one arrival a half
+    uint64_t full[8], empty[8];           // the ring's stages; empty and q_empty: one arrival a half
     uint64_t q, q_empty;
     uint64_t s[2], p[2][kParts], o[2];     // scores complete, weights stored, output complete
     uint64_t item[2], item_empty[2], want, next, drain;
@@ -352,7 +369,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (int i = 0; i < ST; ++i) {
             mbar_init(smem_u32(&bars.full[i]), 1);
             mbar_init(smem_u32(&bars.empty[i]), 2);
-            mbar_init(smem_u32(&bars.clean[i]), 1);
         }
         mbar_init(smem_u32(&bars.q), 1);
         mbar_init(smem_u32(&bars.q_empty), 2);
@@ -393,7 +409,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     };
     // Parities: an item's first ring stage, tile of half i, ... is counted over all items of the CTA.
     uint32_t base = 0, tiles0 = 0, tiles1 = 0, worked = 0;  // stages, tiles of each half, items with keys
-    auto advance = [&](const Range &r) {
+    auto advance = [&](const Item &r) {
         base += 2 * (r.jb - r.ja);
         tiles0 += r.jb0 - r.ja;
         tiles1 += r.jb1 - r.ja;
@@ -419,6 +435,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 it.split = int(rest % a.splits);
                 it.valid = find_item(a, rest / a.splits, 2 * a.per_half, lane, it);  // no tile: no later block has one
             }
+            if (it.valid) set_range(a, it);
             if (lane == 0) {
                 it.odd = 0;
                 items[k & 1] = it;
@@ -442,25 +459,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         }
         Item it;
         for (int k = 0; get_item(k, it); ++k) {
-            const Range r = range_of(a, it);
-            auto clean = [&](int j) {  // after tile j's copy has arrived
-                if ((j + 1) * kKeys <= r.vis_lo) return;
-                const uint32_t n = base + 2 * (j - r.ja) + 1, stg = n % ST;
-                ok = warp_wait(smem_u32(&bars.full[stg]), (n / ST) & 1, abort);
-                if (!ok) return;
-                const bool odd = clean_values<T, DP>(raw + (sm0 - smem_u32(raw)) + (2 + stg) * P::kTile,
-                                                     max(r.vis_lo - j * kKeys, 0), min(it.lk - j * kKeys, kKeys), lane);
-                if (lane == 0) {
-                    if (odd) items[k & 1].odd = 1;
-                    mbar_arrive(smem_u32(&bars.clean[stg]));
-                }
-                __syncwarp();
-            };
-            if (r.jb > r.ja) {
+            if (it.jb > it.ja) {
                 if (worked > 0) ok = warp_wait(smem_u32(&bars.q_empty), (worked - 1) & 1, abort);
                 if (ok && lane == 0) {
                     const uint32_t bar = smem_u32(&bars.q), box = uint32_t(a.group * a.per_half) * 128;
-                    const bool half[2] = {r.jb0 > r.ja, r.jb1 > r.ja};
+                    const bool half[2] = {it.jb0 > it.ja, it.jb1 > it.ja};
                     mbar_arrive_expect_tx(bar, box * (DP / 64) * (uint32_t(half[0]) + uint32_t(half[1])));
                     for (int i = 0; i < 2; ++i)
                         for (int b = 0; b < DP / 64; ++b)
@@ -470,9 +473,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 }
                 __syncwarp();
             }
-            for (int j = r.ja; j < r.jb && ok; ++j) {
+            for (int j = it.ja; j < it.jb && ok; ++j) {
                 for (int kv = 0; kv < 2 && ok; ++kv) {
-                    const uint32_t n = base + 2 * (j - r.ja) + kv, stg = n % ST;
+                    const uint32_t n = base + 2 * (j - it.ja) + kv, stg = n % ST;
                     if (n >= ST) ok = warp_wait(smem_u32(&bars.empty[stg]), (n / ST - 1) & 1, abort);
                     if (ok && lane == 0) {
                         const uint32_t bar = smem_u32(&bars.full[stg]);
@@ -484,12 +487,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     if (ok) issued = n + 1;
                     __syncwarp();
                 }
-                // a tile is cleaned once the next one's copies are under way
-                if (ok && j > r.ja) clean(j - 1);
             }
             if (lane == 0) mbar_arrive(smem_u32(&bars.want));
-            if (ok && r.jb > r.ja) clean(r.jb - 1);
-            advance(r);
+            advance(it);
             if (!ok) break;
             done_with_item(k);
         }
@@ -519,17 +519,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         };
         Item it;
         for (int k = 0; ok && get_item(k, it); ++k) {
-            const Range r = range_of(a, it);
-            if (r.jb > r.ja) {
+            if (it.jb > it.ja) {
                 ok = spin_wait(smem_u32(&bars.q), worked & 1, abort) &&
                      spin_wait(smem_u32(&bars.full[base % ST]), (base / ST) & 1, abort);
                 tc_fence_after();
-                if (ok && r.jb0 > r.ja) qk(0, base);
-                if (ok && r.jb1 > r.ja) qk(1, base);
+                if (ok && it.jb0 > it.ja) qk(0, base);
+                if (ok && it.jb1 > it.ja) qk(1, base);
             }
 #pragma unroll 1
-            for (int turn = 0; ok && turn < 2 * (r.jb - r.ja); ++turn) {
-                const int i = turn & 1, j = turn >> 1, left = (i ? r.jb1 : r.jb0) - r.ja - j;
+            for (int turn = 0; ok && turn < 2 * (it.jb - it.ja); ++turn) {
+                const int i = turn & 1, j = turn >> 1, left = (i ? it.jb1 : it.jb0) - it.ja - j;
                 if (left <= 0) continue;
                 const uint32_t n = base + 2 * j + 1, tile = (i ? tiles1 : tiles0) + j;
                 const uint64_t vd = vd0 + uint32_t((n % ST) * P::kTile >> 4);
@@ -551,7 +550,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 else if (elect_one()) mma_commit(smem_u32(&bars.o[i]));
                 __syncwarp();
             }
-            advance(r);
+            advance(it);
             if (ok) done_with_item(k);
         }
         if (*abort) {  // let what was issued end before the tensor memory is freed
@@ -561,46 +560,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         }
     } else {
         // ------------------------------------------------ gate (warp 10): V_j and K_{j+1} have arrived
-        // One arrival of each half's weight barrier, so that the issuer waits for nothing else, and
-        // the releases of a half that does not take part.
+        // One arrival of each half's weight barrier, so that the issuer waits for nothing else, after
+        // V rows that not every row sees are cleaned, and the releases of a half that takes no part.
         bool ok = true;
-        uint32_t cleans = 0;  // the parity of each stage's clean barrier
         Item it;
         for (int k = 0; ok && get_item(k, it); ++k) {
-            const Range r = range_of(a, it);
             auto arrived = [&](uint32_t n) {
                 ok = ok && warp_wait(smem_u32(&bars.full[n % ST]), (n / ST) & 1, abort);
             };
-            if (r.jb > r.ja) {
+            if (it.jb > it.ja) {
                 arrived(base);
-                if (r.jb0 == r.ja || r.jb1 == r.ja) {
+                if (it.jb0 == it.ja || it.jb1 == it.ja) {
                     ok = ok && warp_wait(smem_u32(&bars.q), worked & 1, abort);
                     if (ok && lane == 0) mbar_arrive(smem_u32(&bars.q_empty));
                 }
             }
-            for (int j = r.ja; j < r.jb && ok; ++j) {
-                const uint32_t n = base + 2 * (j - r.ja) + 1, stg = n % ST;
+            for (int j = it.ja; j < it.jb && ok; ++j) {
+                const uint32_t n = base + 2 * (j - it.ja) + 1, stg = n % ST;
                 arrived(n);
-                if (ok && (j + 1) * kKeys > r.vis_lo) {
-                    ok = warp_wait(smem_u32(&bars.clean[stg]), (cleans >> stg) & 1, abort);
-                    cleans ^= 1u << stg;
-                }
-                if (j + 1 < r.jb) arrived(n + 1);
+                if (ok && (j + 1) * kKeys > it.vis_lo &&
+                    clean_values<T, DP>(raw + (sm0 - smem_u32(raw)) + (2 + stg) * P::kTile,
+                                        max(it.vis_lo - j * kKeys, 0), min(it.lk - j * kKeys, kKeys), lane) &&
+                    lane == 0)
+                    items[k & 1].odd = 1;
+                if (j + 1 < it.jb) arrived(n + 1);
                 for (int i = 0; i < 2 && ok; ++i) {
-                    if (j >= (i ? r.jb1 : r.jb0)) {
+                    if (j >= (i ? it.jb1 : it.jb0)) {
                         if (lane == 0) {
                             mbar_arrive(smem_u32(&bars.empty[(n - 1) % ST]));
                             mbar_arrive(smem_u32(&bars.empty[stg]));
                         }
                         continue;
                     }
-                    const uint32_t tile = (i ? tiles1 : tiles0) + (j - r.ja);
+                    const uint32_t tile = (i ? tiles1 : tiles0) + (j - it.ja);
                     if (tile > 0) ok = warp_wait(smem_u32(&bars.p[i][0]), (tile - 1) & 1, abort);
                     if (ok && lane == 0) mbar_arrive(smem_u32(&bars.p[i][0]));
                 }
                 __syncwarp();
             }
-            advance(r);
+            advance(it);
             if (ok) done_with_item(k);
         }
     }
@@ -614,6 +612,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 256 + i * DP;
         const bool releases = (tid & 127) == 0;
+        const int mine = (tid & 127) / a.group;  // this row's token within the half
         uint32_t tiles = 0, outputs = 0;  // tiles of this half so far, items in which it took part
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -624,12 +623,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             int count, stages, vis, vis_half;
             {
                 const Item it = items[k & 1];
-                const Range r = range_of(a, it);
-                count = (i ? r.jb1 : r.jb0) - r.ja;
-                stages = 2 * (r.jb - r.ja);
-                const int first = it.t0 + i * a.per_half, mine = (tid & 127) / a.group, t = first + mine;
-                vis = (mine < a.per_half && t < it.lq ? visible(a, it, t) : 0) - r.ja * kKeys;
-                vis_half = visible(a, it, first) - r.ja * kKeys;
+                count = (i ? it.jb1 : it.jb0) - it.ja;
+                stages = 2 * (it.jb - it.ja);
+                const int t = it.t0 + i * a.per_half + mine;
+                vis = (mine < a.per_half && t < it.lq ? visible(a, it, t) : 0) - it.ja * kKeys;
+                vis_half = (i ? it.vis_lo1 : it.vis_lo) - it.ja * kKeys;
             }
             float top = -INFINITY, sum0 = 0.f, sum1 = 0.f;
 #pragma unroll 1
@@ -717,7 +715,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             if (ok) {
                 tc_fence_after();
                 const Item it = items[k & 1];
-                const int mine = (tid & 127) / a.group, t = it.t0 + i * a.per_half + mine;
+                const int t = it.t0 + i * a.per_half + mine;
                 const bool row_valid = mine < a.per_half && t < it.lq;
                 const float sum = count > 0 ? sum0 + sum1 : 0.f;
                 const bool none = !(sum != 0.f);  // no key seen (a NaN sum is not none)
@@ -725,46 +723,80 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 const int head = it.hk * a.group + (tid & 127) - mine * a.group;
                 const int64_t row = (int64_t(it.q0) + t) * a.shape.hq + head;
                 const bool odd = count > 0 && it.odd;
+                // The warp's 32 rows go through its own shared memory, 128 bytes of each at a time, so
+                // that 8 lanes write one row's 128 bytes (a lane writing its own row takes 4 times as
+                // long); out_row: where this lane's row goes, in elements of what is stored.
+                uint8_t *stage = raw + (sm0 - smem_u32(raw)) + P::kOut + warp * 4096;
+                const int64_t out_row = !row_valid ? -1
+                                        : a.part   ? (int64_t(it.split) * a.tokens_q * a.shape.hq + row) * a.shape.d
+                                                   : (int64_t(it.q0) + t) * a.so.t + head * a.so.h;
+                int64_t to[8];  // of the rows that this lane helps to write
 #pragma unroll
-                for (int c = 0; c < DP / 32; ++c) {
-                    float o[32];
-                    if (count > 0) {
-                        tmem_ld_32x32b_x32(o_addr + c * 32, o);
-                        tmem_ld_wait();
-                        loaded(o);
-                    }
+                for (int e = 0; e < 8; ++e) to[e] = __shfl_sync(0xffffffffu, out_row, 4 * e + (lane >> 3));
+                // 16-byte unit u of row r sits at unit u ^ (r & 7): no bank conflicts either way
+                auto unit = [&](int r, int u) { return reinterpret_cast<uint4 *>(stage + r * 128 + ((u ^ (r & 7)) << 4)); };
+                auto load_o = [&](int col, float(&o)[32]) {
+                    tmem_ld_32x32b_x32(o_addr + col, o);
+                    tmem_ld_wait();
+                    loaded(o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
-                    if (!row_valid || c * 32 >= a.shape.d) continue;
-                    if (odd) {
-                        const Range r = range_of(a, it);
-                        const int odd_from = max(r.vis_lo, r.ja * kKeys);
-                        const int odd_to = min(visible(a, it, t), (r.ja + count) * kKeys);
-                        const T *v = static_cast<const T *>(a.v_data) + it.hk * a.sv.h + c * 32;
-                        for (int key = odd_from; key < odd_to; ++key) {
-                            const T *vr = v + (int64_t(it.k0) + key) * a.sv.t;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                if (c * 32 + e >= a.shape.d) continue;
-                                const float x = float(vr[e]);
-                                if (!isfinite(x)) o[e] += x;
-                            }
+                };
+                // Non-finite values that were taken out of V, for the row that this lane staged: the first
+                // element `col`, n elements of type E.
+                auto add_odd = [&](int col, int n, auto *first_elem) {
+                    using E = typename std::remove_pointer<decltype(first_elem)>::type;
+                    const int from = max(it.vis_lo, it.ja * kKeys);
+                    const int end = min(visible(a, it, t), (it.ja + count) * kKeys);
+                    const T *v = static_cast<const T *>(a.v_data) + it.hk * a.sv.h;
+#pragma unroll 1
+                    for (int key = from; key < end; ++key)
+#pragma unroll 1
+                        for (int e = col; e < min(col + n, a.shape.d); ++e) {
+                            const float x = float(v[(int64_t(it.k0) + key) * a.sv.t + e]);
+                            if (isfinite(x)) continue;
+                            const int per_unit = 16 / int(sizeof(E));
+                            E *p = reinterpret_cast<E *>(unit(lane, (e - col) / per_unit)) + (e - col) % per_unit;
+                            *p = E(float(*p) + x);
                         }
-                    }
-                    if (!a.part) {
-                        T *dst = static_cast<T *>(a.out) + (int64_t(it.q0) + t) * a.so.t + head * a.so.h + c * 32;
+                };
+                auto write = [&](auto *dst, int col) {
+                    __syncwarp();
+                    uint4 x[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            if (c * 32 + e < a.shape.d)
-                                *reinterpret_cast<uint4 *>(dst + e) =
+                    for (int e = 0; e < 8; ++e) x[e] = *unit(4 * e + (lane >> 3), lane & 7);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (to[e] >= 0 && col < a.shape.d) *reinterpret_cast<uint4 *>(dst + to[e] + col) = x[e];
+                    __syncwarp();
+                };
+                if (!a.part) {
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 64) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float o[32];
+                            load_o(c + h * 32, o);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                *unit(lane, h * 4 + e / 8) =
                                     make_uint4(pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
                                                pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
-                    } else {
-                        float *dst = a.part + (int64_t(it.split) * a.tokens_q * a.shape.hq + row) * a.shape.d + c * 32;
+                        }
+                        if (odd && row_valid) add_odd(c, 64, static_cast<T *>(nullptr));
+                        write(static_cast<T *>(a.out), c + (lane & 7) * 8);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 32) {
+                        float o[32];
+                        load_o(c, o);
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            if (c * 32 + e < a.shape.d)
-                                *reinterpret_cast<float4 *>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                            *unit(lane, e / 4) = make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]),
+                                                            __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3]));
+                        if (odd && row_valid) add_odd(c, 32, static_cast<float *>(nullptr));
+                        write(a.part, c + (lane & 7) * 4);
                     }
                 }
                 if (row_valid) {
