@@ -43,13 +43,12 @@ constexpr int kTcThreads = 384;  // 168 registers each at launch: 64512 in all
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56;  // 256 * 224 + 128 * 56 = 64512
 constexpr float kSlack = 8.0f;  // how far (in powers of two) a row's scores may pass its maximum
 
-// Shared-memory plan for a padded head size DP: Q_0, Q_1, a ring of K and V tiles, and 4 KB a
-// softmax warp for its output rows.  A tile is DP/64 blocks of 128 rows x 128 bytes, 128-byte swizzled.
+// Shared-memory plan for a padded head size DP: Q_0, Q_1, then a ring of K and V tiles.  A tile
+// is DP/64 blocks of 128 rows x 128 bytes, 128-byte swizzled.
 template <int DP> struct Plan {
     static constexpr int kTile = kRows * DP * 2;
-    static constexpr int kStages = DP == 128 ? 4 : 8;
-    static constexpr int kOut = (2 + kStages) * kTile;
-    static constexpr size_t kBytes = size_t(kOut) + 8 * 4096 + 1024;
+    static constexpr int kStages = DP == 128 ? 5 : 8;
+    static constexpr size_t kBytes = size_t(2 + kStages) * kTile + 1024;
 };
 
 struct TcArgs {
@@ -112,6 +111,29 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// Lane l holds 128 bytes of row l, unit u (16 bytes) in x[u]; afterwards x[e] of lane l is unit l / 4
+// of row 4 e + l % 4, so that a warp's store of x[e] writes four rows' 128 bytes whole (a lane that
+// writes its own row touches a line of its own with every store: 4 times as long for the tile).
+// An 8 x 8 transposition: the unit's bits change places with the row's upper bits, one a step.
+__device__ __forceinline__ void rows_to_lines(uint4 (&x)[8], int lane) {
+#pragma unroll
+    for (int bit = 4; bit; bit >>= 1) {
+        const bool upper = lane & (bit * 4);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (u & bit) continue;
+            uint4 &lo = x[u], &hi = x[u | bit];
+            uint4 give = upper ? lo : hi;
+            give.x = __shfl_xor_sync(0xffffffffu, give.x, bit * 4);
+            give.y = __shfl_xor_sync(0xffffffffu, give.y, bit * 4);
+            give.z = __shfl_xor_sync(0xffffffffu, give.z, bit * 4);
+            give.w = __shfl_xor_sync(0xffffffffu, give.w, bit * 4);
+            if (upper) lo = give;
+            else hi = give;
+        }
+    }
+}
+
 // Operand whose rows run along the MMA's K and whose contiguous side is M or N (V): 64-element
 // blocks lbo bytes apart, groups of 8 rows 1024 bytes apart, 128-byte swizzle.
 __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t addr, uint32_t lbo_bytes) {
@@ -139,7 +161,7 @@ __device__ __forceinline__ void seq_bounds(const int32_t *cu, int64_t s, int64_t
 
 // One sequence's query tiles of `span` tokens.
 struct Tiles {
-    int q0, lq, lk, count;
+    int q0, lq, k0, lk, count;
 
     // The first of its tiles whose last token sees keys of at least x key tiles, `count` if there is
     // none; the tiles after it see at least as many.
@@ -147,18 +169,17 @@ struct Tiles {
         const int64_t keys = int64_t(kKeys) * (x - 1) + 1;
         if (x <= 0) return 0;
         if (lk < keys) return count;
-        if (!causal) return 0;
-        return int(max((keys - lk + lq + span - 1) / span - 1, int64_t(0)));
+        const int64_t last = causal ? keys - lk + lq : 0;  // the last token that a tile has to reach, less 1: at most lq
+        return last <= span ? 0 : int((unsigned(last) + unsigned(span) - 1) / unsigned(span)) - 1;
     }
 };
 
 __device__ __forceinline__ Tiles tiles_of(const TcArgs &a, int64_t s, int span) {
-    Tiles t = {0, 0, 0, 0};
-    if (s < a.n_seqs) {
-        int k0;
+    Tiles t = {0, 0, 0, 0, 0};
+    if (a.cu_q && s < a.n_seqs) {
         seq_bounds(a.cu_q, s, a.tokens_q, t.q0, t.lq);
-        seq_bounds(a.cu_k, s, a.tokens_k, k0, t.lk);
-        t.count = int((int64_t(t.lq) + span - 1) / span);
+        seq_bounds(a.cu_k, s, a.tokens_k, t.k0, t.lk);
+        t.count = int((unsigned(t.lq) + unsigned(span) - 1) / unsigned(span));
     }
     return t;
 }
@@ -167,16 +188,16 @@ __device__ __forceinline__ Tiles tiles_of(const TcArgs &a, int64_t s, int span) 
 // short ones), or for many sequences, where that search would take longer than it saves, the
 // last sequence's last tile first.  One warp; false when there is no such tile.
 constexpr int kSortedSeqs = 32;
-__device__ __forceinline__ bool find_item(const TcArgs &a, int64_t rank, int span, int lane, Item &it) {
+__device__ __forceinline__ bool find_item(const TcArgs &a, unsigned rank, int span, int lane, const Tiles &own, Item &it) {
     if (!a.cu_q) {
         it.q0 = it.k0 = 0;
         it.lq = int(a.tokens_q);
         it.lk = int(a.tokens_k);
-        it.t0 = int(rank * span);
-        return rank * span < a.tokens_q;
+        it.t0 = int(rank) * span;
+        return int64_t(rank) * span < a.tokens_q;
     }
-    if (a.n_seqs <= kSortedSeqs) {
-        const Tiles t = tiles_of(a, lane, span);
+    if (a.n_seqs <= kSortedSeqs) {  // lane l holds sequence l
+        const Tiles &t = own;
         if (rank >= __reduce_add_sync(0xffffffffu, unsigned(t.count))) return false;
         // the largest x for which more than `rank` tiles see at least x key tiles
         int lo = 0, hi = int(__reduce_max_sync(0xffffffffu, unsigned(t.lk)) / kKeys) + 2;
@@ -200,13 +221,13 @@ __device__ __forceinline__ bool find_item(const TcArgs &a, int64_t rank, int spa
         it.q0 = __shfl_sync(0xffffffffu, t.q0, src);
         it.lq = __shfl_sync(0xffffffffu, t.lq, src);
         it.t0 = int(__shfl_sync(0xffffffffu, unsigned(first) - before, src) + left) * span;
-        seq_bounds(a.cu_k, src, a.tokens_k, it.k0, it.lk);
+        it.k0 = __shfl_sync(0xffffffffu, t.k0, src);
+        it.lk = __shfl_sync(0xffffffffu, t.lk, src);
         return true;
     }
     int64_t before = 0;
     for (int64_t s0 = (a.n_seqs - 1) / 32 * 32; s0 >= 0; s0 -= 32) {  // lane l: the l'th sequence from the chunk's end
-        const int64_t s = s0 + 31 - lane;
-        const Tiles t = tiles_of(a, s, span);
+        const Tiles t = tiles_of(a, s0 + 31 - lane, span);
         unsigned incl = unsigned(t.count);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -220,7 +241,8 @@ __device__ __forceinline__ bool find_item(const TcArgs &a, int64_t rank, int spa
             it.q0 = __shfl_sync(0xffffffffu, t.q0, src);
             it.lq = __shfl_sync(0xffffffffu, t.lq, src);
             it.t0 = int(__shfl_sync(0xffffffffu, int(last - 1 - rank), src)) * span;
-            seq_bounds(a.cu_k, s0 + 31 - src, a.tokens_k, it.k0, it.lk);
+            it.k0 = __shfl_sync(0xffffffffu, t.k0, src);
+            it.lk = __shfl_sync(0xffffffffu, t.lk, src);
             return true;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
@@ -422,6 +444,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         // ------------------------------------------------ items: this block's, then blocks that have not started
         int64_t id = blockIdx.x;
         int asked = 0;
+        const Tiles own = tiles_of(a, lane, 2 * a.per_half);
         for (int k = 0;; ++k) {
             if (k >= 2 && !warp_wait(smem_u32(&bars.item_empty[k & 1]), ((k >> 1) - 1) & 1, abort)) break;
             Item it;
@@ -429,11 +452,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             if (id >= 0) {
                 if (id == 0 && lane == 0) *a.status = QMM_OK;  // long before a wait can give up
                 // blocks in order: all heads and splits of a tile, then the next tile
-                int64_t rest = id;
-                it.hk = int(rest % a.shape.hk);
-                rest /= a.shape.hk;
-                it.split = int(rest % a.splits);
-                it.valid = find_item(a, rest / a.splits, 2 * a.per_half, lane, it);  // no tile: no later block has one
+                const unsigned rest = unsigned(id) / unsigned(a.shape.hk), rank = rest / unsigned(a.splits);
+                it.hk = int(unsigned(id) - rest * unsigned(a.shape.hk));
+                it.split = int(rest - rank * unsigned(a.splits));
+                it.valid = find_item(a, rank, 2 * a.per_half, lane, own, it);  // no tile: no later block has one
             }
             if (it.valid) set_range(a, it);
             if (lane == 0) {
@@ -723,80 +745,69 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 const int head = it.hk * a.group + (tid & 127) - mine * a.group;
                 const int64_t row = (int64_t(it.q0) + t) * a.shape.hq + head;
                 const bool odd = count > 0 && it.odd;
-                // The warp's 32 rows go through its own shared memory, 128 bytes of each at a time, so
-                // that 8 lanes write one row's 128 bytes (a lane writing its own row takes 4 times as
-                // long); out_row: where this lane's row goes, in elements of what is stored.
-                uint8_t *stage = raw + (sm0 - smem_u32(raw)) + P::kOut + warp * 4096;
+                // where this lane's row goes, in elements of what is stored; of the rows that it helps to write
                 const int64_t out_row = !row_valid ? -1
                                         : a.part   ? (int64_t(it.split) * a.tokens_q * a.shape.hq + row) * a.shape.d
                                                    : (int64_t(it.q0) + t) * a.so.t + head * a.so.h;
-                int64_t to[8];  // of the rows that this lane helps to write
+                int64_t to[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) to[e] = __shfl_sync(0xffffffffu, out_row, 4 * e + (lane >> 3));
-                // 16-byte unit u of row r sits at unit u ^ (r & 7): no bank conflicts either way
-                auto unit = [&](int r, int u) { return reinterpret_cast<uint4 *>(stage + r * 128 + ((u ^ (r & 7)) << 4)); };
+                for (int e = 0; e < 8; ++e) to[e] = __shfl_sync(0xffffffffu, out_row, 4 * e + (lane & 3));
                 auto load_o = [&](int col, float(&o)[32]) {
                     tmem_ld_32x32b_x32(o_addr + col, o);
                     tmem_ld_wait();
                     loaded(o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
-                };
-                // Non-finite values that were taken out of V, for the row that this lane staged: the first
-                // element `col`, n elements of type E.
-                auto add_odd = [&](int col, int n, auto *first_elem) {
-                    using E = typename std::remove_pointer<decltype(first_elem)>::type;
-                    const int from = max(it.vis_lo, it.ja * kKeys);
-                    const int end = min(visible(a, it, t), (it.ja + count) * kKeys);
-                    const T *v = static_cast<const T *>(a.v_data) + it.hk * a.sv.h;
+                    if (odd && row_valid) {  // non-finite values that were taken out of V
+                        const int from = max(it.vis_lo, it.ja * kKeys);
+                        const int end = min(visible(a, it, t), (it.ja + count) * kKeys);
+                        const T *v = static_cast<const T *>(a.v_data) + it.hk * a.sv.h + col;
 #pragma unroll 1
-                    for (int key = from; key < end; ++key)
-#pragma unroll 1
-                        for (int e = col; e < min(col + n, a.shape.d); ++e) {
-                            const float x = float(v[(int64_t(it.k0) + key) * a.sv.t + e]);
-                            if (isfinite(x)) continue;
-                            const int per_unit = 16 / int(sizeof(E));
-                            E *p = reinterpret_cast<E *>(unit(lane, (e - col) / per_unit)) + (e - col) % per_unit;
-                            *p = E(float(*p) + x);
-                        }
-                };
-                auto write = [&](auto *dst, int col) {
-                    __syncwarp();
-                    uint4 x[8];
+                        for (int key = from; key < end; ++key)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = *unit(4 * e + (lane >> 3), lane & 7);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (to[e] >= 0 && col < a.shape.d) *reinterpret_cast<uint4 *>(dst + to[e] + col) = x[e];
-                    __syncwarp();
+                            for (int e = 0; e < 32; ++e) {
+                                if (col + e >= a.shape.d) continue;
+                                const float x = float(v[(int64_t(it.k0) + key) * a.sv.t + e]);
+                                if (!isfinite(x)) o[e] += x;
+                            }
+                    }
                 };
                 if (!a.part) {
 #pragma unroll 1
                     for (int c = 0; c < DP; c += 64) {
+                        uint4 x[8];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float o[32];
                             load_o(c + h * 32, o);
 #pragma unroll
                             for (int e = 0; e < 32; e += 8)
-                                *unit(lane, h * 4 + e / 8) =
+                                x[h * 4 + e / 8] =
                                     make_uint4(pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
                                                pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
                         }
-                        if (odd && row_valid) add_odd(c, 64, static_cast<T *>(nullptr));
-                        write(static_cast<T *>(a.out), c + (lane & 7) * 8);
+                        rows_to_lines(x, lane);
+                        const int col = c + (lane >> 2) * 8;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (to[e] >= 0 && col < a.shape.d)
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to[e] + col) = x[e];
                     }
                 } else {
 #pragma unroll 1
                     for (int c = 0; c < DP; c += 32) {
                         float o[32];
                         load_o(c, o);
+                        uint4 x[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *unit(lane, e / 4) = make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]),
-                                                            __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3]));
-                        if (odd && row_valid) add_odd(c, 32, static_cast<float *>(nullptr));
-                        write(a.part, c + (lane & 7) * 4);
+                        for (int e = 0; e < 8; ++e)
+                            x[e] = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                                              __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+                        rows_to_lines(x, lane);
+                        const int col = c + (lane >> 2) * 4;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (to[e] >= 0 && col < a.shape.d) *reinterpret_cast<uint4 *>(a.part + to[e] + col) = x[e];
                     }
                 }
                 if (row_valid) {
