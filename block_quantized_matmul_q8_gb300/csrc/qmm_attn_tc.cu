@@ -111,23 +111,25 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// Lane l holds 128 bytes of row l, unit u (16 bytes) in x[u]; afterwards x[e] of lane l is unit l / 4
-// of row 4 e + l % 4, so that a warp's store of x[e] writes four rows' 128 bytes whole (a lane that
-// writes its own row touches a line of its own with every store: 4 times as long for the tile).
-// An 8 x 8 transposition: the unit's bits change places with the row's upper bits, one a step.
-__device__ __forceinline__ void rows_to_lines(uint4 (&x)[8], int lane) {
+// Lane l holds N 16-byte units of row l, unit u in x[u]; afterwards x[e] of lane l is unit
+// l * N / 32 of row (32 / N) * e + l % (32 / N), so that a warp's store of x[e] writes whole pieces
+// of N units of 32 / N rows (a lane that writes its own row touches a line of its own with every
+// store, and the tile takes 3 to 4 times as long).  An N x N transposition: the unit's bits change
+// places with the row's upper bits, one a step.
+template <int N> __device__ __forceinline__ void rows_to_pieces(uint4 (&x)[N], int lane) {
 #pragma unroll
-    for (int bit = 4; bit; bit >>= 1) {
-        const bool upper = lane & (bit * 4);
+    for (int bit = N / 2; bit; bit >>= 1) {
+        const int other = bit * (32 / N);
+        const bool upper = lane & other;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < N; ++u) {
             if (u & bit) continue;
             uint4 &lo = x[u], &hi = x[u | bit];
             uint4 give = upper ? lo : hi;
-            give.x = __shfl_xor_sync(0xffffffffu, give.x, bit * 4);
-            give.y = __shfl_xor_sync(0xffffffffu, give.y, bit * 4);
-            give.z = __shfl_xor_sync(0xffffffffu, give.z, bit * 4);
-            give.w = __shfl_xor_sync(0xffffffffu, give.w, bit * 4);
+            give.x = __shfl_xor_sync(0xffffffffu, give.x, other);
+            give.y = __shfl_xor_sync(0xffffffffu, give.y, other);
+            give.z = __shfl_xor_sync(0xffffffffu, give.z, other);
+            give.w = __shfl_xor_sync(0xffffffffu, give.w, other);
             if (upper) lo = give;
             else hi = give;
         }
@@ -373,7 +375,8 @@ __device__ __forceinline__ int64_t take_next_block(uint4 *answer, uint32_t bar, 
     return yes ? int64_t(id) : -1;
 }
 
-template <typename T, int DP>
+// kPartial: fp32 partial rows of a key split instead of the output.
+template <typename T, int DP, bool kPartial>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ TcArgs a) {
     using P = Plan<DP>;
     constexpr int ST = P::kStages;
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     sum0 *= f;
                     sum1 *= f;
                     // S_i(j) was issued after O_i's last product, so that one is done
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < DP / 16; ++c) {
                         float o[16];
                         tmem_ld_32x32b_x16(o_addr + c * 16, o);
@@ -746,14 +749,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 const int64_t row = (int64_t(it.q0) + t) * a.shape.hq + head;
                 const bool odd = count > 0 && it.odd;
                 // where this lane's row goes, in elements of what is stored; of the rows that it helps to write
+                using Out = typename std::conditional<kPartial, float, T>::type;
+                constexpr int kUnits = 32 * int(sizeof(Out)) / 16;  // of 32 elements
+                Out *const out = kPartial ? reinterpret_cast<Out *>(a.part) : static_cast<Out *>(a.out);
                 const int64_t out_row = !row_valid ? -1
-                                        : a.part   ? (int64_t(it.split) * a.tokens_q * a.shape.hq + row) * a.shape.d
+                                        : kPartial ? (int64_t(it.split) * a.tokens_q * a.shape.hq + row) * a.shape.d
                                                    : (int64_t(it.q0) + t) * a.so.t + head * a.so.h;
-                int64_t to[8];
+                int64_t to[kUnits];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) to[e] = __shfl_sync(0xffffffffu, out_row, 4 * e + (lane & 3));
-                auto load_o = [&](int col, float(&o)[32]) {
-                    tmem_ld_32x32b_x32(o_addr + col, o);
+                for (int e = 0; e < kUnits; ++e)
+                    to[e] = __shfl_sync(0xffffffffu, out_row, (32 / kUnits) * e + (lane & (32 / kUnits - 1)));
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 32) {  // rolled: code that runs once an item is fetched anew each time
+                    float o[32];
+                    tmem_ld_32x32b_x32(o_addr + c, o);
                     tmem_ld_wait();
                     loaded(o);
 #pragma unroll
@@ -761,58 +770,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     if (odd && row_valid) {  // non-finite values that were taken out of V
                         const int from = max(it.vis_lo, it.ja * kKeys);
                         const int end = min(visible(a, it, t), (it.ja + count) * kKeys);
-                        const T *v = static_cast<const T *>(a.v_data) + it.hk * a.sv.h + col;
+                        const T *v = static_cast<const T *>(a.v_data) + it.hk * a.sv.h + c;
 #pragma unroll 1
                         for (int key = from; key < end; ++key)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                if (col + e >= a.shape.d) continue;
+                                if (c + e >= a.shape.d) continue;
                                 const float x = float(v[(int64_t(it.k0) + key) * a.sv.t + e]);
                                 if (!isfinite(x)) o[e] += x;
                             }
                     }
-                };
-                if (!a.part) {
-#pragma unroll 1
-                    for (int c = 0; c < DP; c += 64) {
-                        uint4 x[8];
+                    uint4 x[kUnits];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float o[32];
-                            load_o(c + h * 32, o);
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                x[h * 4 + e / 8] =
-                                    make_uint4(pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
-                                               pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
-                        }
-                        rows_to_lines(x, lane);
-                        const int col = c + (lane >> 2) * 8;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (to[e] >= 0 && col < a.shape.d)
-                                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to[e] + col) = x[e];
-                    }
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < DP; c += 32) {
-                        float o[32];
-                        load_o(c, o);
-                        uint4 x[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < kUnits; ++e) {
+                        if (kPartial)
                             x[e] = make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
                                               __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
-                        rows_to_lines(x, lane);
-                        const int col = c + (lane >> 2) * 4;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (to[e] >= 0 && col < a.shape.d) *reinterpret_cast<uint4 *>(a.part + to[e] + col) = x[e];
+                        else
+                            x[e] = make_uint4(pack2<T>(o[8 * e], o[8 * e + 1]), pack2<T>(o[8 * e + 2], o[8 * e + 3]),
+                                              pack2<T>(o[8 * e + 4], o[8 * e + 5]), pack2<T>(o[8 * e + 6], o[8 * e + 7]));
                     }
+                    rows_to_pieces(x, lane);
+                    const int col = c + lane / (32 / kUnits) * (32 / kUnits);
+#pragma unroll
+                    for (int e = 0; e < kUnits; ++e)
+                        if (to[e] >= 0 && col < a.shape.d) *reinterpret_cast<uint4 *>(out + to[e] + col) = x[e];
                 }
                 if (row_valid) {
                     const float l2 = none ? -INFINITY : top * a.scale_log2 + log2f(sum);
-                    if (a.part) a.part_lse[int64_t(it.split) * a.tokens_q * a.shape.hq + row] = l2;
+                    if (kPartial) a.part_lse[int64_t(it.split) * a.tokens_q * a.shape.hq + row] = l2;
                     else if (a.lse) a.lse[row] = l2 * kLn2;
                 }
             }
@@ -830,7 +816,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 }
 
 template <typename T, int DP> cudaError_t launch_dp(const TcArgs &a, int64_t blocks, cudaStream_t st) {
-    auto kern = attn_tc_kernel<T, DP>;
+    auto kern = a.part ? attn_tc_kernel<T, DP, true> : attn_tc_kernel<T, DP, false>;
     cudaError_t e = ensure_smem(kern, Plan<DP>::kBytes);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)blocks, kTcThreads, Plan<DP>::kBytes, st>>>(a);
