@@ -4,9 +4,11 @@
 //
 // Bound by HBM: each element is read once and written once.  One block takes one token (or a
 // share of its heads when there are few tokens); its first threads compute the token's
-// rotary/2 angles once for all heads while the first heads are being loaded.  Four
-// consecutive elements sit in one lane, so that a head's sum of squares is a shuffle
-// reduction over at most 32 lanes and the partner half of a rotated pair is one shuffle away.
+// rotary/2 angles once for all heads while the first heads are being loaded.  A lane holds eight
+// elements of a head, four of them the partners of the other four, so that a pair turns inside a
+// lane and a head's sum of squares is a reduction over at most 16 lanes (with four elements a lane
+// and the partner a shuffle away the arithmetic took longer than the traffic: 90 against 62 us for
+// 8192 tokens of 40 + 8 + 8 fp32 heads of 128).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,9 +22,8 @@ namespace qmm {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeBatch = 4;  // heads whose loads a warp has in flight
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 __device__ __forceinline__ float4 load4(const __half *p) {
@@ -47,6 +48,28 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
         make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
+// Sine and cosine of pos * freq.  The angle is taken in turns as a 64-bit fraction, whose whole
+// turns fall off by themselves: freq / (2 pi) = m 2^q / (2 pi) for freq's mantissa m, with 1 / (2 pi)
+// as a 64-bit integer over 2^66, times pos modulo 2^64.  Exact to 2^-32 of a turn at every int32 position.
+__device__ __forceinline__ float2 cos_sin(int pos, float freq) {
+    const uint32_t bits = __float_as_uint(freq), expo = (bits >> 23) & 255u;
+    const uint64_t m = (bits & 0x7fffffu) | (expo ? 0x800000u : 0u);
+    const int q = int(expo ? expo : 1u) - 150;
+    constexpr uint64_t kInv2Pi = 0xA2F9836E4E44152Aull;  // round(2^66 / (2 pi))
+    const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+    const int right = 2 - q;  // turns per position in units of 2^-64: (hi:lo) 2^-right
+    uint64_t f;
+    if (right <= 0) f = right > -64 ? lo << -right : 0;
+    else if (right < 64) f = (hi << (64 - right)) | (lo >> right);
+    else f = right < 128 ? hi >> (right - 64) : 0;
+    uint64_t turns = f * uint64_t(int64_t(pos));
+    if (bits >> 31) turns = 0 - turns;
+    float s, c;
+    sincospif(float(int32_t(turns >> 32)) * 4.6566128730773926e-10f, &s, &c);  // 2^-31: half turns
+    if (expo == 255u) s = c = __int_as_float(0x7fffffff);
+    return make_float2(c, s);
+}
+
 template <typename In, typename Out>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a, int lanes_log2, int share) {
     __shared__ float2 cs[kMaxHeadDim / 2];
@@ -54,113 +77,80 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
     const int64_t t = blockIdx.x;
     const int d = a.shape.d, hq = a.shape.hq, hk = a.shape.hk, r = a.rotary;
     const int lanes = 1 << lanes_log2;                // lanes of one head
-    const int sub = lane >> lanes_log2, c = lane & (lanes - 1), e0 = 4 * c;
+    const int sub = lane >> lanes_log2, c = lane & (lanes - 1);
     const int per_warp = 32 >> lanes_log2;            // heads of one warp at a time
     const int total = hq + (a.v ? 2 : 1) * hk;
     const int h_begin = blockIdx.y * share, h_end = min(total, h_begin + share);
-    const bool live = e0 < d;
+    const bool live = 8 * c < d, turned = 8 * c < r;
+    // this lane's elements e0..e0+3 and e1..e1+3: pairs across them, or within each when interleaved
+    const int e0 = turned && !a.interleaved ? 4 * c : 8 * c, e1 = turned && !a.interleaved ? r / 2 + 4 * c : 8 * c + 4;
 
-    auto load = [&](int h) -> float4 {
-        if (!live || h >= h_end) return make_float4(0.f, 0.f, 0.f, 0.f);
-        const In *p;
-        if (h < hq) p = static_cast<const In *>(a.q) + t * a.sq.t + h * a.sq.h;
-        else if (h < hq + hk) p = static_cast<const In *>(a.k) + t * a.sk.t + (h - hq) * a.sk.h;
-        else p = static_cast<const In *>(a.v) + t * a.sv.t + (h - hq - hk) * a.sv.h;
-        return load4(p + e0);
+    auto load = [&](int h, float4 &x, float4 &y) {
+        x = y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!live || h >= h_end) return;
+        const In *p = h < hq        ? static_cast<const In *>(a.q) + t * a.sq.t + h * a.sq.h
+                      : h < hq + hk ? static_cast<const In *>(a.k) + t * a.sk.t + (h - hq) * a.sk.h
+                                    : static_cast<const In *>(a.v) + t * a.sv.t + (h - hq - hk) * a.sv.h;
+        x = load4(p + e0);
+        y = load4(p + e1);
     };
-    float4 x[kRopeBatch];
-    int h0 = h_begin + warp * per_warp + sub;
+    int h = h_begin + warp * per_warp + sub;
     const int step = kRopeWarps * per_warp;
-#pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) x[i] = load(h0 + i * step);
-
-    if (tid < r / 2) {
-        // the angle in turns, reduced in fp64: exact to about 1e-7 rad at every int32 position
-        const double turns = double(a.positions[t]) * double(a.inv_freq[tid]) * 0.15915494309189533577;
-        float s, co;
-        sincospif(2.0f * float(turns - rint(turns)), &s, &co);
-        cs[tid] = make_float2(co, s);
-    }
-    float4 wq = make_float4(1.f, 1.f, 1.f, 1.f), wk = wq;
-    if (live && a.wq) wq = make_float4(a.wq[e0], a.wq[e0 + 1], a.wq[e0 + 2], a.wq[e0 + 3]);
-    if (live && a.wk) wk = make_float4(a.wk[e0], a.wk[e0 + 1], a.wk[e0 + 2], a.wk[e0 + 3]);
+    float4 x, y;
+    load(h, x, y);
+    if (tid < r / 2) cs[tid] = cos_sin(a.positions[t], a.inv_freq[tid]);
     __syncthreads();
-
-    // this lane's cosines and sines: out = n * co + partner * si, element by element
-    float co[4] = {1.f, 1.f, 1.f, 1.f}, si[4] = {0.f, 0.f, 0.f, 0.f};
-    int partner = lane;
-    if (e0 < r) {
-        if (a.interleaved) {
+    float2 turn[4];  // of the lane's four pairs
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 v = cs[2 * c + j];
-                co[2 * j] = co[2 * j + 1] = v.x;
-                si[2 * j] = -v.y;
-                si[2 * j + 1] = v.y;
-            }
-        } else {
-            const int half = r / 8;  // lanes of the first half (r is a multiple of 8)
-            const bool first = c < half;
-            partner = first ? lane + half : lane - half;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 v = cs[e0 + j - (first ? 0 : r / 2)];
-                co[j] = v.x;
-                si[j] = first ? -v.y : v.y;
-            }
-        }
-    }
+    for (int j = 0; j < 4; ++j) turn[j] = turned ? cs[4 * c + j] : make_float2(1.f, 0.f);
     const float inv_d = 1.0f / float(d);
 
-    for (; h0 - sub < h_end; h0 += kRopeBatch * step) {
-#pragma unroll
-        for (int i = 0; i < kRopeBatch; ++i) {
-            const int h = h0 + i * step;
-            float4 n = x[i];
-            const bool is_q = h < hq, is_k = !is_q && h < hq + hk;
-            float ss = n.x * n.x + n.y * n.y + n.z * n.z + n.w * n.w;
-            for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if ((is_q && a.wq) || (is_k && a.wk)) {
-                const float inv = rsqrtf(ss * inv_d + a.eps);
-                const float4 w = is_q ? wq : wk;
-                n.x = n.x * inv * w.x;
-                n.y = n.y * inv * w.y;
-                n.z = n.z * inv * w.z;
-                n.w = n.w * inv * w.w;
-            }
-            float4 p;
-            if (a.interleaved) {
-                p = make_float4(n.y, n.x, n.w, n.z);
-            } else {
-                p.x = __shfl_sync(0xffffffffu, n.x, partner);
-                p.y = __shfl_sync(0xffffffffu, n.y, partner);
-                p.z = __shfl_sync(0xffffffffu, n.z, partner);
-                p.w = __shfl_sync(0xffffffffu, n.w, partner);
-            }
-            if (live && h < h_end) {
-                Out *out;
-                if (is_q) out = static_cast<Out *>(a.qo) + t * a.sqo.t + h * a.sqo.h;
-                else if (is_k) out = static_cast<Out *>(a.ko) + t * a.sko.t + (h - hq) * a.sko.h;
-                else out = static_cast<Out *>(a.vo) + t * a.svo.t + (h - hq - hk) * a.svo.h;
-                if ((is_q || is_k) && e0 < r) {
-                    n.x = n.x * co[0] + p.x * si[0];
-                    n.y = n.y * co[1] + p.y * si[1];
-                    n.z = n.z * co[2] + p.z * si[2];
-                    n.w = n.w * co[3] + p.w * si[3];
-                }
-                store4(out + e0, n);
-            }
-            x[i] = load(h + kRopeBatch * step);
+    for (; h - sub < h_end; h += step) {
+        float4 A = x, B = y;
+        load(h + step, x, y);
+        const bool is_q = h < hq, is_v = h >= hq + hk;
+        const float *w = is_v ? nullptr : is_q ? a.wq : a.wk;
+        float ss = A.x * A.x + A.y * A.y + A.z * A.z + A.w * A.w + B.x * B.x + B.y * B.y + B.z * B.z + B.w * B.w;
+        for (int o = lanes >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (!live || h >= h_end) continue;
+        if (w) {  // read again for every head: from the L1 cache, where registers would cost occupancy
+            const float inv = rsqrtf(ss * inv_d + a.eps);
+            A = make_float4(A.x * inv * w[e0], A.y * inv * w[e0 + 1], A.z * inv * w[e0 + 2], A.w * inv * w[e0 + 3]);
+            B = make_float4(B.x * inv * w[e1], B.y * inv * w[e1 + 1], B.z * inv * w[e1 + 2], B.w * inv * w[e1 + 3]);
         }
+        if (!is_v && turned) {
+            auto rotate = [](float &p, float &q, float2 cs) {
+                const float n = p * cs.x - q * cs.y;
+                q = q * cs.x + p * cs.y;
+                p = n;
+            };
+            if (a.interleaved) {
+                rotate(A.x, A.y, turn[0]);
+                rotate(A.z, A.w, turn[1]);
+                rotate(B.x, B.y, turn[2]);
+                rotate(B.z, B.w, turn[3]);
+            } else {
+                rotate(A.x, B.x, turn[0]);
+                rotate(A.y, B.y, turn[1]);
+                rotate(A.z, B.z, turn[2]);
+                rotate(A.w, B.w, turn[3]);
+            }
+        }
+        Out *out = is_q    ? static_cast<Out *>(a.qo) + t * a.sqo.t + h * a.sqo.h
+                   : !is_v ? static_cast<Out *>(a.ko) + t * a.sko.t + (h - hq) * a.sko.h
+                           : static_cast<Out *>(a.vo) + t * a.svo.t + (h - hq - hk) * a.svo.h;
+        store4(out + e0, A);
+        store4(out + e1, B);
     }
 }
 
 template <typename In, typename Out> cudaError_t launch_typed(const RopeArgs &a, cudaStream_t st) {
-    const int lanes_log2 = a.shape.d > 64 ? 5 : a.shape.d > 32 ? 4 : 3;
+    int lanes_log2 = 0;
+    while ((8 << lanes_log2) < a.shape.d) ++lanes_log2;
     const int total = a.shape.hq + (a.v ? 2 : 1) * a.shape.hk;
     // few tokens: the heads of a token are shared among blocks, one round of a block's warps each
     const int round = kRopeWarps * (32 >> lanes_log2);
-    const int share = a.m < 2 * device_sm_count() ? round : total;
+    const int share = a.m < 4 * device_sm_count() ? round : (total + round - 1) / round * round;
     const dim3 grid((unsigned)a.m, (unsigned)((total + share - 1) / share));
     qk_norm_rope_kernel<In, Out><<<grid, kRopeThreads, 0, st>>>(a, lanes_log2, share);
     return cudaGetLastError();

@@ -387,7 +387,7 @@ typedef struct {
  *   the pairs (a, b) = (n[i], n[i + rotary_dim/2]), or (n[2i], n[2i+1]) when interleaved,
  *   i < rotary_dim/2, turn by the angle positions[t] * inv_freq[i]:
  *   (a cos - b sin, b cos + a sin); the other elements stay.
- * The angle is reduced in fp64, so it is as exact at position 2^31 - 1 as at 1.
+ * The angle is reduced as a 64-bit fraction of a turn, so it is as exact at position 2^31 - 1 as at 1.
  *   q, k, v   : in_type (QMM_F32, QMM_F16 or QMM_BF16) [m] tokens of heads_q, heads_kv and
  *               heads_kv heads; v (with v_out) may be NULL.
  *   w_q, w_k  : fp32 [head_dim], or NULL for no norm.
