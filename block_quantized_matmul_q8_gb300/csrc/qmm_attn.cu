@@ -14,7 +14,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "qmm_attn.cuh"
 #include "qmm_internal.h"
@@ -409,8 +408,15 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 3) att
         }
         const float *src = a.part + (row0 + row) * d.shape.d + col;
         const int64_t step = all_rows * d.shape.d;
-#pragma unroll 4
-        for (int p = 0; p < a.parts; ++p) add(pweight_s[row][p], __ldcg(reinterpret_cast<const float4 *>(src + p * step)));
+        for (int p0 = 0; p0 < a.parts; p0 += 8) {  // eight loads in flight: the join waits for nothing else
+            float4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = __ldcg(reinterpret_cast<const float4 *>(src + min(p0 + i, a.parts - 1) * step));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (p0 + i < a.parts) add(pweight_s[row][p0 + i], x[i]);
+        }
         T *out = static_cast<T *>(d.out) + b * d.so.t + (head0 + row) * d.so.h + col;
         *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
     }
@@ -419,19 +425,24 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 3) att
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Whether the prefix goes through the tensor-core phase: the rows of the batch that share a kv
-// head are many enough that reading the prefix once for all of them pays for a second launch.
+// Whether the prefix goes through the tensor-core phase.  Read inline, every request reads it
+// again from L2; read once for all, it costs a second launch and the join of partial rows.  Even
+// where the rereading comes to about 70 MB (32/8 heads of 128, prefix and requests: 1000 x 8, 33 MB,
+// 9.5 us inline and 11.7 on the tensor cores; 1000 x 16, 66 MB, 12.8 and 12.0; 1000 x 32, 131 MB,
+// 18.3 and 12.7; 8192 x 64, 190 and 35).
 bool prefix_on_tensor_cores(const DecodeArgs &d) {
-    if (getenv("X_TC")) return d.prefix > 0 && atoi(getenv("X_TC"));
-    return d.prefix > 0 && d.batch * d.prefix > 16384;
+    return 4.0 * double(d.batch) * double(d.shape.hk) * double(d.prefix) * double(d.shape.d) > 80e6;
 }
 
-// CTAs of one request and kv head: enough for every SM to hold several, two tiles each.
+// CTAs of one request and kv head (a power of two, at most one for each key tile): as many as
+// leave every CTA resident at once with room to spare (two an SM: a grid of clusters that nearly
+// fills the SMs runs its last clusters on their own; 112 pairs of 19 tiles: 9.8 us with 2 CTAs
+// each, 13.3 with 4), or, for long caches, parts of at least 32 tiles, which level out ragged
+// lengths (48 x 8 pairs of up to 128 tiles: 140 us with 1, 129 with 4).
 int cluster_ctas(const DecodeArgs &d, int64_t inline_prefix, int64_t pairs) {
     const int64_t tiles = (inline_prefix + kTileKeys - 1) / kTileKeys + (d.room + kTileKeys - 1) / kTileKeys;
     int c = 1;
-    if (getenv("X_C")) return atoi(getenv("X_C"));
-    while (c < kMaxCluster && pairs * c < 6 * device_sm_count() && tiles >= 2 * c) c *= 2;
+    while (c < kMaxCluster && tiles >= 2 * c && (pairs * 2 * c <= 2 * device_sm_count() || tiles >= 64 * c)) c *= 2;
     return c;
 }
 

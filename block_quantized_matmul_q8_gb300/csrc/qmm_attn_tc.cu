@@ -23,7 +23,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cstdlib>
 #include <type_traits>
 
 #include "qmm_attn.cuh"
@@ -883,7 +882,6 @@ int attn_prefix_splits(const DecodeArgs &d) {
     const int64_t span = 2 * (kRows / (d.shape.hq / d.shape.hk));
     const int64_t pairs = (d.batch + span - 1) / span * d.shape.hk, tiles = (d.prefix + kKeys - 1) / kKeys;
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>({device_sm_count() / pairs, tiles / 2, int64_t(kMaxPrefixParts)}));
-    if (getenv("X_S")) return std::min<int64_t>(tiles, atoi(getenv("X_S")));
     const int64_t per = (tiles + most - 1) / most;
     return int((tiles + per - 1) / per);
 }
