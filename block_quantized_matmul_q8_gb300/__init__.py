@@ -12,6 +12,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+import threading
 
 import torch
 
@@ -452,44 +454,73 @@ def qmm_get_device_status(workspace: torch.Tensor, stream=None) -> int:
     return int(lib().qmm_get_device_status(_ptr(workspace), _stream(stream)))
 
 
-def _heads(t: torch.Tensor, name: str, shape=None, dtype=None) -> Heads:
-    """The qmm_heads of a CUDA tensor whose last three dimensions are [tokens, heads, head_dim]."""
+class _Views(threading.local):
+    """Room for the qmm_heads of one call, of this thread: filled and read within the call."""
+
+    def __init__(self):
+        self.words = (ctypes.c_int64 * 18)()
+        first = ctypes.addressof(self.words)
+        self.at = tuple(ctypes.cast(first + 24 * i, ctypes.POINTER(Heads)) for i in range(6))
+
+
+_views = _Views()
+_pack4, _pack6 = (struct.Struct(f"{3 * n}q").pack_into for n in (4, 6))
+
+
+def _view(t: torch.Tensor, name: str, shape, dtype):
+    """(data, token stride, head stride) of a CUDA tensor whose last three dimensions are
+    [tokens, heads, head_dim], after checking its type and shape."""
     if not t.is_cuda:
         raise QMMError(1, f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise QMMError(3, f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
+    if t.shape != shape:
         raise QMMError(2, f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise QMMError(1, f"{name}: the elements of a head must be contiguous")
-    return Heads(t.data_ptr(), st[-3], st[-2])
+    return t.data_ptr(), st[-3], st[-2]
 
 
 def _small(t, name, dtype, numel):
     """A contiguous CUDA tensor of `numel` elements (or None), as a pointer."""
     if t is None:
         return None
-    _dev(t, name, dtype)
+    if not t.is_cuda or t.dtype is not dtype or not t.is_contiguous():
+        _dev(t, name, dtype)
     if t.numel() != numel:
         raise QMMError(2, f"{name} must have {numel} elements, got {t.numel()}")
     return t.data_ptr()
 
 
-def _scratch(need, workspace, device):
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    return _dev(workspace, "workspace")
+_status_words = {}
+
+
+def _scratch(need, workspace, like):
+    """(workspace, pointer, bytes, whether it was made for this call).  Where a call needs no more
+    than its status word and the caller gave no workspace, one block for each device takes it."""
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size(), False
+    if need > 256:
+        workspace = like.new_empty(need, dtype=torch.uint8)
+        return workspace, workspace.data_ptr(), need, True
+    device = like.get_device()
+    block = _status_words.get(device)
+    if block is None:
+        block = _status_words[device] = torch.empty(256, dtype=torch.uint8, device=like.device)
+    return block, block.data_ptr(), 256, False
 
 
 def _on_stream(stream, *made):
     """The stream's handle; tensors that a call made for itself are kept until that stream is done with them."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     for t in made:
-        t.record_stream(stream)
+        if t is not None:
+            t.record_stream(stream)
     return stream.cuda_stream
 
 
@@ -504,28 +535,35 @@ def qmm_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None, p
     outputs may be views of a cache."""
     if q.dim() != 3 or k.dim() != 3:
         raise QMMError(2, "q and k must be [tokens, heads, head_dim]")
-    m, hq, d = q.shape
+    shape, dtype = q.shape, q.dtype
+    m, hq, d = shape
     hk = k.shape[1]
-    if q_out is None:
-        q_out = torch.empty((m, hq, d), dtype=out_dtype, device=q.device)
-    if k_out is None:
-        k_out = torch.empty((m, hk, d), dtype=out_dtype, device=q.device)
-    if v is not None and v_out is None:
-        v_out = torch.empty((m, hk, d), dtype=out_dtype, device=q.device)
-    if q.dtype not in FLOATS or out_dtype not in FLOATS:
+    if dtype not in FLOATS or out_dtype not in FLOATS:
         raise QMMError(3, "q must be fp32, fp16 or bf16")
     kv = (m, hk, d)
-    args = [_heads(q, "q"), _heads(k, "k", kv, q.dtype), None if v is None else _heads(v, "v", kv, q.dtype),
-            _heads(q_out, "q_out", q.shape, out_dtype), _heads(k_out, "k_out", kv, out_dtype),
-            None if v is None else _heads(v_out, "v_out", kv, out_dtype)]
-    rotary = 0 if inv_freq is None else 2 * inv_freq.numel()
-    _check(lib().qmm_qk_norm_rope(args[0], args[1], args[2], FLOATS[q.dtype], m, hq, hk, d,
-                                  _small(w_q, "w_q", torch.float32, d), _small(w_k, "w_k", torch.float32, d), eps,
+    made = [None, None, None]
+    if q_out is None:
+        made[0] = q_out = torch.empty_like(q, dtype=out_dtype, memory_format=torch.contiguous_format)
+    if k_out is None:
+        made[1] = k_out = torch.empty_like(k, dtype=out_dtype, memory_format=torch.contiguous_format)
+    if v is not None and v_out is None:
+        made[2] = v_out = torch.empty_like(v, dtype=out_dtype, memory_format=torch.contiguous_format)
+    words, at = _views.words, _views.at
+    if v is None:
+        _pack4(words, 0, *_view(q, "q", shape, dtype), *_view(k, "k", kv, dtype),
+               *_view(q_out, "q_out", shape, out_dtype), *_view(k_out, "k_out", kv, out_dtype))
+        q_, k_, v_, qo, ko, vo = at[0], at[1], None, at[2], at[3], None
+    else:
+        _pack6(words, 0, *_view(q, "q", shape, dtype), *_view(k, "k", kv, dtype), *_view(v, "v", kv, dtype),
+               *_view(q_out, "q_out", shape, out_dtype), *_view(k_out, "k_out", kv, out_dtype),
+               *_view(v_out, "v_out", kv, out_dtype))
+        q_, k_, v_, qo, ko, vo = at
+    half = 0 if inv_freq is None else inv_freq.numel()
+    _check(lib().qmm_qk_norm_rope(q_, k_, v_, FLOATS[dtype], m, hq, hk, d, _small(w_q, "w_q", torch.float32, d),
+                                  _small(w_k, "w_k", torch.float32, d), eps,
                                   _small(positions, "positions", torch.int32, m),
-                                  _small(inv_freq, "inv_freq", torch.float32, rotary // 2), rotary, int(interleaved),
-                                  args[3], args[4], args[5], FLOATS[out_dtype],
-                                  _on_stream(stream, q_out, k_out, *(() if v is None else (v_out,)))),
-           "qmm_qk_norm_rope")
+                                  _small(inv_freq, "inv_freq", torch.float32, half), 2 * half, interleaved, qo, ko, vo,
+                                  FLOATS[out_dtype], _on_stream(stream, *made)), "qmm_qk_norm_rope")
     return q_out, k_out, v_out
 
 
@@ -542,29 +580,36 @@ def qmm_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     or bf16, cu_q and cu_k int32 [n_seqs + 1] row bounds (cu_k None: the same as cu_q)."""
     if q.dim() != 3 or k.dim() != 3:
         raise QMMError(2, "q and k must be [tokens, heads, head_dim]")
-    (tq, hq, d), (tk, hk, _) = q.shape, k.shape
-    if q.dtype not in FLOATS:
+    shape, dtype = q.shape, q.dtype
+    tq, hq, d = shape
+    tk, hk = k.shape[0], k.shape[1]
+    if dtype not in FLOATS:
         raise QMMError(3, "q must be fp16 or bf16")
-    made = out is None
-    if made:
-        out = torch.empty((tq, hq, d), dtype=q.dtype, device=q.device)
+    made = None
+    if out is None:
+        made = out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    kv = (tk, hk, d)
+    _pack4(_views.words, 0, *_view(q, "q", shape, dtype), *_view(k, "k", kv, dtype), *_view(v, "v", kv, dtype),
+           *_view(out, "out", shape, dtype))
+    q_, k_, v_, o_ = _views.at[:4]
     n = cu_q.numel() - 1
-    cu_k = cu_q if cu_k is None else cu_k
-    ws = _scratch(qmm_workspace_bytes_attn_prompt(tq, tk, n, hq, hk, d), workspace, q.device)
-    _check(lib().qmm_attn_prompt(_heads(q, "q"), _heads(k, "k", (tk, hk, d), q.dtype),
-                                 _heads(v, "v", (tk, hk, d), q.dtype), FLOATS[q.dtype], tq, tk, hq, hk, d,
-                                 _small(cu_q, "cu_q", torch.int32, n + 1), _small(cu_k, "cu_k", torch.int32, n + 1), n,
-                                 int(causal), d ** -0.5 if scale is None else scale,
-                                 _heads(out, "out", q.shape, q.dtype), _small(lse, "lse", torch.float32, tq * hq),
-                                 ws.data_ptr(), ws.numel() * ws.element_size(),
-                                 _on_stream(stream, *((ws,) if workspace is None else ()), *((out,) if made else ()))),
-           "qmm_attn_prompt")
+    bounds_q = _small(cu_q, "cu_q", torch.int32, n + 1)
+    bounds_k = bounds_q if cu_k is None else _small(cu_k, "cu_k", torch.int32, n + 1)
+    L = lib()
+    ws, ws_ptr, ws_bytes, ws_made = _scratch(L.qmm_workspace_bytes_attn_prompt(tq, tk, n, hq, hk, d), workspace, q)
+    _check(L.qmm_attn_prompt(q_, k_, v_, FLOATS[dtype], tq, tk, hq, hk, d, bounds_q, bounds_k, n, causal,
+                             d ** -0.5 if scale is None else scale, o_,
+                             None if lse is None else _small(lse, "lse", torch.float32, tq * hq), ws_ptr, ws_bytes,
+                             _on_stream(stream, made, ws if ws_made else None)), "qmm_attn_prompt")
     return out
 
 
 def qmm_workspace_bytes_attn_decode(batch: int, room: int, prefix_len: int, heads_q: int, heads_kv: int,
                                     head_dim: int) -> int:
     return lib().qmm_workspace_bytes_attn_decode(batch, room, prefix_len, heads_q, heads_kv, head_dim)
+
+
+_NO_VIEW = (0, 0, 0)
 
 
 def qmm_attn_decode(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | None, lens: torch.Tensor | None,
@@ -575,30 +620,40 @@ def qmm_attn_decode(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | N
     that all requests share and the caches k and v [batch, room, kv_heads, d] with lens int32 [batch]."""
     if q.dim() != 3 or (k is None and prefix_k is None):
         raise QMMError(2, "q must be [batch, heads, head_dim], with caches or a prefix")
-    b, hq, d = q.shape
-    if q.dtype not in FLOATS:
+    shape, dtype = q.shape, q.dtype
+    b, hq, d = shape
+    if dtype not in FLOATS:
         raise QMMError(3, "q must be fp16 or bf16")
-    if k is not None and k.dim() != 4:
-        raise QMMError(2, "k must be [batch, room, kv_heads, head_dim]")
-    hk = (k if k is not None else prefix_k).shape[-2]
-    room = 0 if k is None else k.shape[1]
-    p = 0 if prefix_k is None else prefix_k.shape[0]
-    kh = vh = pk = pv = None
+    for pair, what in (((k, v), "k and v"), ((prefix_k, prefix_v), "prefix_k and prefix_v")):
+        if (pair[0] is None) != (pair[1] is None):
+            raise QMMError(1, f"{what} go together")
+    room = p = kb = vb = 0
+    kh = vh = pk = pv = _NO_VIEW
     if k is not None:
-        kh, vh = (_heads(x, n, (b, room, hk, d), q.dtype) for x, n in ((k, "k"), (v, "v")))
+        if k.dim() != 4:
+            raise QMMError(2, "k must be [batch, room, kv_heads, head_dim]")
+        room, hk = k.shape[1], k.shape[2]
+        cache = (b, room, hk, d)
+        kh, vh = _view(k, "k", cache, dtype), _view(v, "v", cache, dtype)
+        kb, vb = k.stride(0), v.stride(0)
     if prefix_k is not None:
-        pk, pv = (_heads(x, n, (p, hk, d), q.dtype) for x, n in ((prefix_k, "prefix_k"), (prefix_v, "prefix_v")))
-    made = out is None
-    if made:
-        out = torch.empty((b, hq, d), dtype=q.dtype, device=q.device)
-    ws = _scratch(qmm_workspace_bytes_attn_decode(b, room, p, hq, hk, d), workspace, q.device)
-    _check(lib().qmm_attn_decode(_heads(q, "q"), kh, vh, 0 if k is None else k.stride(0),
-                                 0 if k is None else v.stride(0), _small(lens, "lens", torch.int32, b), b, room, pk, pv,
-                                 p, FLOATS[q.dtype], hq, hk, d, d ** -0.5 if scale is None else scale,
-                                 _heads(out, "out", q.shape, q.dtype), _small(lse, "lse", torch.float32, b * hq),
-                                 ws.data_ptr(), ws.numel() * ws.element_size(),
-                                 _on_stream(stream, *((ws,) if workspace is None else ()), *((out,) if made else ()))),
-           "qmm_attn_decode")
+        if prefix_k.dim() != 3:
+            raise QMMError(2, "prefix_k must be [prefix_len, kv_heads, head_dim]")
+        p = prefix_k.shape[0]
+        if k is None:
+            hk = prefix_k.shape[1]
+        pk, pv = _view(prefix_k, "prefix_k", (p, hk, d), dtype), _view(prefix_v, "prefix_v", (p, hk, d), dtype)
+    made = None
+    if out is None:
+        made = out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    _pack6(_views.words, 0, *_view(q, "q", shape, dtype), *kh, *vh, *pk, *pv, *_view(out, "out", shape, dtype))
+    q_, k_, v_, pk_, pv_, o_ = _views.at
+    L = lib()
+    ws, ws_ptr, ws_bytes, ws_made = _scratch(L.qmm_workspace_bytes_attn_decode(b, room, p, hq, hk, d), workspace, q)
+    _check(L.qmm_attn_decode(q_, k_, v_, kb, vb, _small(lens, "lens", torch.int32, b), b, room, pk_, pv_, p,
+                             FLOATS[dtype], hq, hk, d, d ** -0.5 if scale is None else scale, o_,
+                             None if lse is None else _small(lse, "lse", torch.float32, b * hq), ws_ptr, ws_bytes,
+                             _on_stream(stream, made, ws if ws_made else None)), "qmm_attn_decode")
     return out
 
 
