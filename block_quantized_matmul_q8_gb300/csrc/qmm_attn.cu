@@ -40,7 +40,7 @@ template <int DP> struct Ring {
     static constexpr int kPartStride = DP + 4;        // floats between a warp's partial rows
     static constexpr size_t kBytes = size_t(kStages) * kTile + 1024;
     static constexpr int kParts = kWarps * kMaxRows * kPartStride;  // floats of the CTA's partial rows
-    static_assert((kParts + kMaxRows * (kMaxCluster + kMaxPrefixParts + 2)) * 4 <= kStages * kTile,
+    static_assert((kParts + kMaxRows * (kMaxCluster + kMaxSplits + 2)) * 4 <= kStages * kTile,
                   "partial rows and weights reuse the ring");
 };
 
@@ -310,7 +310,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 3) att
     float *part = reinterpret_cast<float *>(raw + (sm - smem_u32(raw)));
     // weights of the partial rows in the join: the cluster's CTAs and the tensor-core phase's splits
     auto weight_s = reinterpret_cast<float(*)[kMaxCluster + 1]>(part + R::kParts);
-    auto pweight_s = reinterpret_cast<float(*)[kMaxPrefixParts + 1]>(weight_s + kMaxRows);
+    auto pweight_s = reinterpret_cast<float(*)[kMaxSplits + 1]>(weight_s + kMaxRows);
     if (warp < kWarps) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {

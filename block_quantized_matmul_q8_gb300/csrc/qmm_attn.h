@@ -60,9 +60,11 @@ struct DecodeArgs {
     int64_t batch, room, prefix;
     float scale;
 };
+// Largest number of key splits of the tensor-core kernel.
+constexpr int kMaxSplits = 64;
+
 // The prefix phase of a decode call on the tensor cores: normalised fp32 partial rows
 // [splits][batch * hq][d] and their log2 denominators [splits][batch * hq].
-constexpr int kMaxPrefixParts = 64;
 int attn_prefix_splits(const DecodeArgs &a);
 cudaError_t launch_attn_prefix(const DecodeArgs &a, qmm_float t, int splits, float *part, float *part_lse, void *ws,
                                cudaStream_t st);

@@ -814,6 +814,63 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
+// The joined output row of a prompt call with key splits: out = sum_s 2^(lse_s) part_s / sum_s 2^(lse_s),
+// one warp a row, four elements a lane.
+template <typename T> __global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ TcArgs a) {
+    const int lane = threadIdx.x & 31, d = a.shape.d;
+    const int64_t rows = a.tokens_q * a.shape.hq, row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int64_t t = row / a.shape.hq;
+    const int h = int(row - t * a.shape.hq);
+    bool mine = false;  // whether some sequence holds this query: other rows are not written
+    for (int64_t s = lane; s < a.n_seqs; s += 32) {
+        int q0, lq;
+        seq_bounds(a.cu_q, s, a.tokens_q, q0, lq);
+        mine |= t >= q0 && t < int64_t(q0) + lq;
+    }
+    if (!__any_sync(0xffffffffu, mine)) return;
+    grid_dependency_wait();
+    float l[2], top = -INFINITY;  // of splits lane and lane + 32
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int s = lane + 32 * i;
+        l[i] = s < a.splits ? a.part_lse[s * rows + row] : -INFINITY;
+        top = fmaxf(top, l[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sum += l[i] = ex2(l[i] - base);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const bool none = !(sum != 0.f);
+    const float inv = none ? 0.f : 1.f / sum;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool live = 4 * lane < d;
+    const float *src = a.part + row * d + (live ? 4 * lane : 0);
+    for (int s0 = 0; s0 < a.splits; s0 += 8) {
+        float4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = __ldcg(reinterpret_cast<const float4 *>(src + int64_t(min(s0 + i, a.splits - 1)) * rows * d));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float w = __shfl_sync(0xffffffffu, s0 < 32 ? l[0] : l[1], (s0 + i) & 31) * inv;
+            if (s0 + i >= a.splits) continue;
+            acc.x += w * x[i].x;
+            acc.y += w * x[i].y;
+            acc.z += w * x[i].z;
+            acc.w += w * x[i].w;
+        }
+    }
+    if (live)
+        *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + t * a.so.t + h * a.so.h + 4 * lane) =
+            make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
+    if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (base + log2f(sum)) * kLn2;
+}
+
 template <typename T, int DP> cudaError_t launch_dp(const TcArgs &a, int64_t blocks, cudaStream_t st) {
     auto kern = a.part ? attn_tc_kernel<T, DP, true> : attn_tc_kernel<T, DP, false>;
     cudaError_t e = ensure_smem(kern, Plan<DP>::kBytes);
@@ -849,7 +906,33 @@ cudaError_t launch_tc(const TcArgs &a, qmm_float t, int64_t blocks, cudaStream_t
 
 }  // namespace
 
-size_t attn_prompt_workspace_bytes(const PromptArgs &) { return 256; }
+namespace {
+
+// Upper bound of a prompt call's query tiles: n sequences of l_i > 0 tokens have
+// sum (floor((l_i - 1) / span) + 1) <= floor((tokens - n) / span) + n, which grows with n.
+int64_t prompt_tiles(const PromptArgs &p) {
+    const int64_t span = 2 * (kRows / (p.shape.hq / p.shape.hk)), n = std::min(p.n_seqs, p.tokens_q);
+    return (p.tokens_q - n) / span + n;
+}
+
+// Key splits of a prompt call: where the tiles would leave half of the SMs or more without work, as
+// many as give each SM an item, of at least four key tiles (counted for sequences of equal lengths:
+// the host does not know theirs).
+int prompt_splits(const PromptArgs &p) {
+    const int64_t items = prompt_tiles(p) * p.shape.hk;
+    if (items == 0 || p.n_seqs == 0) return 1;
+    const int64_t key_tiles = p.tokens_k / p.n_seqs / kKeys;
+    return int(std::max<int64_t>(1, std::min<int64_t>({device_sm_count() / items, key_tiles / 4, kMaxSplits})));
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+}  // namespace
+
+size_t attn_prompt_workspace_bytes(const PromptArgs &p) {
+    const size_t splits = prompt_splits(p), rows = size_t(p.tokens_q) * p.shape.hq;
+    return splits == 1 ? 256 : 256 + align256(splits * rows * p.shape.d * 4) + align256(splits * rows * 4);
+}
 
 cudaError_t launch_attn_prompt(const PromptArgs &p, qmm_float t, void *ws, cudaStream_t st) {
     TcArgs a = common_args(p.shape, t, p.scale, ws);
@@ -871,9 +954,17 @@ cudaError_t launch_attn_prompt(const PromptArgs &p, qmm_float t, void *ws, cudaS
     a.tokens_q = p.tokens_q;
     a.tokens_k = p.tokens_k;
     a.causal = p.causal;
-    // each sequence ends in at most one partial tile, and every tile holds a token
-    const int64_t tiles = std::min(p.tokens_q, p.tokens_q / (2 * a.per_half) + p.n_seqs);
-    return launch_tc(a, t, tiles * p.shape.hk, st);
+    a.splits = prompt_splits(p);
+    const int64_t rows = p.tokens_q * p.shape.hq;
+    if (a.splits > 1) {
+        uint8_t *at = static_cast<uint8_t *>(ws) + 256;
+        a.part = reinterpret_cast<float *>(at);
+        a.part_lse = reinterpret_cast<float *>(at + align256(size_t(a.splits) * rows * p.shape.d * 4));
+    }
+    const cudaError_t e = launch_tc(a, t, prompt_tiles(p) * a.splits * p.shape.hk, st);
+    if (e != cudaSuccess || a.splits == 1) return e;
+    auto join = t == QMM_F16 ? attn_join_kernel<__half> : attn_join_kernel<__nv_bfloat16>;
+    return launch_pdl(join, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a);
 }
 
 // The prefix's key splits: enough CTAs (tiles of queries x kv heads x splits) for every SM, at
@@ -881,7 +972,7 @@ cudaError_t launch_attn_prompt(const PromptArgs &p, qmm_float t, void *ws, cudaS
 int attn_prefix_splits(const DecodeArgs &d) {
     const int64_t span = 2 * (kRows / (d.shape.hq / d.shape.hk));
     const int64_t pairs = (d.batch + span - 1) / span * d.shape.hk, tiles = (d.prefix + kKeys - 1) / kKeys;
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>({device_sm_count() / pairs, tiles / 2, int64_t(kMaxPrefixParts)}));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>({device_sm_count() / pairs, tiles / 2, int64_t(kMaxSplits)}));
     const int64_t per = (tiles + most - 1) / most;
     return int((tiles + per - 1) / per);
 }

@@ -145,6 +145,48 @@ def test_prompt(lq, lk, hq, hk, d, causal, dt):
     check_prompt(q, k, v, lq, lk, causal, d ** -0.5, out, lse)
 
 
+@pytest.mark.parametrize("lq,lk,hq,hk,d,causal,dt", [
+    ([1], [8192], 8, 2, 128, True, BF),                 # one row over many keys
+    ([37, 12], [5000, 900], 8, 1, 64, True, FP),        # sequences with more and with fewer key tiles than splits
+    ([64], [2000], 4, 4, 128, False, BF),
+    ([100, 0, 3], [3000, 2500, 2], 4, 2, 80, True, FP), # a sequence without queries, rows with hardly any key
+    ([30, 20], [4000, 0], 4, 1, 128, True, BF),         # a sequence without keys
+    ([500], [500 * 8 + 1], 8, 1, 64, True, BF),
+])
+def test_prompt_few_rows_many_keys(lq, lk, hq, hk, d, causal, dt):
+    """Calls whose keys are split among SMs and joined: the workspace holds the parts."""
+    assert qmm.qmm_workspace_bytes_attn_prompt(sum(lq), sum(lk), len(lq), hq, hk, d) > 256
+    g = gen(sum(lk) + d)
+    q, k, v = make_prompt(g, lq, lk, hq, hk, d, dt)
+    lse = torch.full((sum(lq), hq), 7.0, device=DEV)
+    out = qmm.qmm_attn_prompt(q, k, v, bounds(lq), bounds(lk), causal=causal, lse=lse)
+    check_prompt(q, k, v, lq, lk, causal, d ** -0.5, out, lse)
+    # the same bits again, with a workspace that holds NaN
+    ws = torch.full((qmm.qmm_workspace_bytes_attn_prompt(sum(lq), sum(lk), len(lq), hq, hk, d),), 255,
+                    dtype=torch.uint8, device=DEV)
+    again = qmm.qmm_attn_prompt(q, k, v, bounds(lq), bounds(lk), causal=causal, workspace=ws)
+    assert torch.equal(again, out) and qmm.qmm_read_device_status(ws) == 0
+
+
+def test_prompt_few_rows_unseen_places():
+    """Split keys: rows outside the sequences are not written, what a row does not see may be NaN."""
+    hq, hk, d, dt = 4, 1, 64, BF
+    g = gen(20)
+    q, k, v = normal(g, 60, hq, d).to(dt), normal(g, 6000, hk, d).to(dt), normal(g, 6000, hk, d).to(dt)
+    cu_q, cu_k = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([5, 25, 45], [100, 3000, 5800]))
+    k[:100], v[:100], k[5800:], v[5800:], q[:5], q[45:] = (math.nan,) * 6
+    k[3000 - 4:3000], v[3000 - 4:3000] = math.inf, math.nan  # the first sequence's last 4 keys: its last 4 rows see them
+    assert qmm.qmm_workspace_bytes_attn_prompt(60, 6000, 2, hq, hk, d) > 256
+    out = torch.full((60, hq, d), 7.0, dtype=dt, device=DEV)
+    lse = torch.full((60, hq), 7.0, device=DEV)
+    qmm.qmm_attn_prompt(q, k, v, cu_q, cu_k, out=out, lse=lse)
+    for x in (out, lse):
+        assert bool((x[:5] == 7.0).all()) and bool((x[45:] == 7.0).all())
+    check_prompt(q, k, v, [16], [2896], True, d ** -0.5, out, at_q=[5], at_k=[100])
+    assert not torch.isfinite(out[21:25]).any()
+    check_prompt(q, k, v, [20], [2800], True, d ** -0.5, out, lse, at_q=[25], at_k=[3000])
+
+
 def test_prompt_many_short_sequences():
     lens = [(7 * i) % 11 for i in range(700)]
     g = gen(5)
@@ -316,6 +358,32 @@ def test_decode(b, room, p, hq, hk, d, dt):
     lse = torch.full((b, hq), 7.0, device=DEV)
     out = qmm.qmm_attn_decode(q, k, v, lens, prefix_k=pk, prefix_v=pv, lse=lse)
     check_decode(q, k, v, lens, pk, pv, d ** -0.5, out, lse)
+
+
+@pytest.mark.parametrize("b,room,p,hq,hk,d,dt", [
+    (16, 30, 2500, 32, 8, 128, BF),
+    (5, 0, 16500, 8, 4, 64, FP),
+    (70, 9, 4700, 10, 2, 40, BF),       # more requests than one tile's rows, 5 heads of one kv head
+    (3, 200, 9001, 28, 4, 128, FP),
+    (160, 66, 1000, 32, 2, 80, BF),
+])
+def test_decode_prefix_read_once(b, room, p, hq, hk, d, dt):
+    """Prefixes about the size from which they go through the tensor-core phase (the workspace then
+    holds its parts)."""
+    assert (qmm.qmm_workspace_bytes_attn_decode(b, room, p, hq, hk, d) > 256) == (4 * b * hk * p * d > 80e6)
+    g = gen(b + p)
+    q, k, v, pk, pv = make_decode(g, b, room, p, hq, hk, d, dt)
+    lens = torch.randint(0, room + 1, (b,), generator=g, device=DEV, dtype=torch.int32) if room else None
+    lse = torch.full((b, hq), 7.0, device=DEV)
+    out = qmm.qmm_attn_decode(q, k, v, lens, prefix_k=pk, prefix_v=pv, lse=lse)
+    check_decode(q, k, v, lens, pk, pv, d ** -0.5, out, lse)
+    ws = torch.full((qmm.qmm_workspace_bytes_attn_decode(b, room, p, hq, hk, d),), 255, dtype=torch.uint8, device=DEV)
+    for scale in (None, -0.2):
+        a, c = (qmm.qmm_attn_decode(q, k, v, lens, prefix_k=pk, prefix_v=pv, workspace=w, scale=scale) for w in (ws, None))
+        assert torch.equal(a, c) and qmm.qmm_read_device_status(ws) == 0
+        if scale is None:
+            assert torch.equal(a, out)
+    check_decode(q, k, v, lens, pk, pv, -0.2, a)
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
