@@ -52,6 +52,7 @@ struct DecArgs {
     int parts;               // partial rows of the tensor-core phase to join
     const float *part, *part_lse;
     float scale_log2;
+    int fault;               // qmm_set_test_fault: no copy is issued, and the waits for them are short
     int *status;
 };
 
@@ -176,7 +177,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 3) att
         bool ok = true;
         int issued = 0;
         if (lane == 0) {
-            for (int i = 0; i < 2 * n && ok; ++i) {
+            for (int i = 0; i < 2 * n && ok && !a.fault; ++i) {
                 const int stg = i % ST, kv = i & 1;
                 if (i >= ST) ok = mbar_wait(smem_u32(&empty[stg]), ((i / ST) - 1) & 1, abort);
                 if (!ok) break;
@@ -221,7 +222,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 3) att
         for (int i = 0; i < n; ++i) {
             const int k_stg = (2 * i) % ST, v_stg = k_stg + 1, phase = ((2 * i) / ST) & 1;
             const uint32_t kt = sm + k_stg * R::kTile, vt = kt + R::kTile;
-            if (!warp_wait(smem_u32(&full[k_stg]), phase, abort)) break;
+            if (!warp_wait(smem_u32(&full[k_stg]), phase, abort, a.fault ? 100000 : kWaitCycles)) break;
             const int64_t j = j0 + i;
             const int64_t left = j < ptiles ? a.inline_prefix - j * kTileKeys : len - (j - ptiles) * kTileKeys;
             const int valid = int(min(left, int64_t(kTileKeys))) - warp * 16;  // of this warp's keys
@@ -486,6 +487,7 @@ cudaError_t launch_attn_decode(const DecodeArgs &d, qmm_float t, void *ws, cudaS
     a.row_blocks = (a.group + kMaxRows - 1) / kMaxRows;
     a.scale_log2 = d.scale * kLog2e;
     a.status = static_cast<int *>(ws);
+    a.fault = test_fault_mode();
     // maps that no tile uses describe q
     const bool cache = d.room > 0, pre = d.prefix > 0;
     if (!attn_make_map(&a.k, t, cache ? d.k : d.q, d.shape.d, cache ? d.shape.hk : 1, cache ? d.room : 1, d.sk, 1,

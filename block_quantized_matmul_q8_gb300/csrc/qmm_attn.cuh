@@ -27,8 +27,9 @@ template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float 
     return r;
 }
 // mbar_wait by a whole warp: all lanes go on, or all give up.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort,
+                                          long long limit = ptx::kWaitCycles) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort, limit));
 }
 
 // A [tokens][heads][d] view (batch of them: batch_stride elements apart) as a tensor map with

@@ -65,6 +65,7 @@ struct TcArgs {
     int causal, splits;
     float scale_log2;       // |scale| * log2(e)
     uint32_t idesc_qk, idesc_pv;
+    int fault;              // qmm_set_test_fault: no copy is issued, and the first wait for one is short
     int *status;
 };
 
@@ -335,13 +336,12 @@ template <typename T, int DP> __device__ __forceinline__ bool clean_values(uint8
     return odd;
 }
 
-constexpr int kParts = 2;      // parts of a tile's weights that are handed over one by one
 constexpr int kItemRoles = 11;  // warps that read an item: softmax, copies, products, gate
 
 struct Bars {
     uint64_t full[8], empty[8];           // the ring's stages; empty and q_empty: one arrival a half
     uint64_t q, q_empty;
-    uint64_t s[2], p[2][kParts], o[2];     // scores complete, weights stored, output complete
+    uint64_t s[2], l[2], p[2][2], o[2];    // scores complete, scores loaded, weights stored, output complete
     uint64_t item[2], item_empty[2], want, next, drain;
 };
 
@@ -379,6 +379,14 @@ template <typename T, int DP, bool kPartial>
 __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_constant__ TcArgs a) {
     using P = Plan<DP>;
     constexpr int ST = P::kStages;
+    // Tensor memory (512 columns): S_0, S_1 (128 each), O_0, O_1 (DP each).  With DP = 128 it is full and
+    // the weights take the place of their scores, so that S(j + 1) waits for the product with V_j.  With
+    // DP = 64 they have columns of their own: S(j + 1) is formed as soon as the softmax has loaded S(j),
+    // and the softmax is never without scores (5 prompt chunks of up to 509 tokens after 3500, 32 heads
+    // of 64: 47.6 -> 36 us).
+    constexpr bool kOwnP = DP == 64;
+    constexpr int kPCol = kOwnP ? 256 + 2 * DP : 0, kPStep = kOwnP ? kKeys / 2 : kKeys;
+    constexpr int kParts = kOwnP ? 1 : 2;  // parts of a tile's weights that are handed over one by one
     extern __shared__ uint8_t raw[];
     __shared__ Bars bars;
     __shared__ Item items[2];
@@ -398,6 +406,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         mbar_init(smem_u32(&bars.q_empty), 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&bars.s[i]), 1);
+            mbar_init(smem_u32(&bars.l[i]), 5);
             for (int h = 0; h < kParts; ++h) mbar_init(smem_u32(&bars.p[i][h]), h == 0 ? 5 : 4);
             mbar_init(smem_u32(&bars.o[i]), 1);
             mbar_init(smem_u32(&bars.item[i]), 1);
@@ -475,7 +484,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     } else if (warp == 8) {
         // ------------------------------------------------ copies
         bool ok = true;
-        uint32_t issued = 0;
+        uint32_t issued = 0, q_issued = 0;
         if (lane == 0) {
             prefetch_tmap(&a.q);
             prefetch_tmap(&a.k);
@@ -485,7 +494,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (int k = 0; get_item(k, it); ++k) {
             if (it.jb > it.ja) {
                 if (worked > 0) ok = warp_wait(smem_u32(&bars.q_empty), (worked - 1) & 1, abort);
-                if (ok && lane == 0) {
+                if (ok && !a.fault) ++q_issued;
+                if (ok && lane == 0 && !a.fault) {
                     const uint32_t bar = smem_u32(&bars.q), box = uint32_t(a.group * a.per_half) * 128;
                     const bool half[2] = {it.jb0 > it.ja, it.jb1 > it.ja};
                     mbar_arrive_expect_tx(bar, box * (DP / 64) * (uint32_t(half[0]) + uint32_t(half[1])));
@@ -501,14 +511,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     const uint32_t n = base + 2 * (j - it.ja) + kv, stg = n % ST;
                     if (n >= ST) ok = warp_wait(smem_u32(&bars.empty[stg]), (n / ST - 1) & 1, abort);
-                    if (ok && lane == 0) {
+                    if (ok && lane == 0 && !a.fault) {
                         const uint32_t bar = smem_u32(&bars.full[stg]);
                         mbar_arrive_expect_tx(bar, P::kTile);
                         for (int b = 0; b < DP / 64; ++b)
                             tma_load_3d(skv + stg * P::kTile + b * kKeys * 128, kv ? &a.v : &a.k, b * 64, it.hk,
                                         it.k0 + j * kKeys, bar);
                     }
-                    if (ok) issued = n + 1;
+                    if (ok && !a.fault) issued = n + 1;
                     __syncwarp();
                 }
             }
@@ -519,7 +529,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         }
         if (*abort) {  // a wait gave up: the copies in flight land before shared memory is released
             int never = 0;
-            if (worked > 0) warp_wait(smem_u32(&bars.q), (worked - 1) & 1, &never);
+            if (q_issued > 0) warp_wait(smem_u32(&bars.q), (q_issued - 1) & 1, &never);
             for (uint32_t n = issued > ST ? issued - ST : 0; n < issued; ++n) {
                 never = 0;
                 warp_wait(smem_u32(&bars.full[n % ST]), (n / ST) & 1, &never);
@@ -527,53 +537,58 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         }
     } else if (warp == 9) {
         // ------------------------------------------------ products, issued by one elected lane
+        // The lane runs an item's whole loop: elected, so that the operands are uniform, and without
+        // the votes and synchronisations of a warp, which would cost as much as the issue.
         bool ok = true;
         const uint64_t qd = smem_desc(sq, 1024, 2), kd0 = smem_desc(skv, 1024, 2), vd0 = smem_desc_mn(skv, kKeys * 128);
         auto qk = [&](int i, uint32_t n) {
             const uint64_t kd = kd0 + uint32_t((n % ST) * P::kTile >> 4);
-            if (elect_one()) {
 #pragma unroll
-                for (int s = 0; s < DP / 16; ++s) {
-                    const uint32_t off = (uint32_t(s / 4) * kRows * 128 + uint32_t(s % 4) * 32) >> 4;
-                    mma_f16(tmem + i * kKeys, qd + uint32_t(i * P::kTile >> 4) + off, kd + off, a.idesc_qk, s != 0);
-                }
-                mma_commit(smem_u32(&bars.s[i]));
+            for (int s = 0; s < DP / 16; ++s) {
+                const uint32_t off = (uint32_t(s / 4) * kRows * 128 + uint32_t(s % 4) * 32) >> 4;
+                mma_f16(tmem + i * kKeys, qd + uint32_t(i * P::kTile >> 4) + off, kd + off, a.idesc_qk, s != 0);
             }
-            __syncwarp();
+            mma_commit(smem_u32(&bars.s[i]));
         };
         Item it;
         for (int k = 0; ok && get_item(k, it); ++k) {
-            if (it.jb > it.ja) {
-                ok = spin_wait(smem_u32(&bars.q), worked & 1, abort) &&
-                     spin_wait(smem_u32(&bars.full[base % ST]), (base / ST) & 1, abort);
-                tc_fence_after();
-                if (ok && it.jb0 > it.ja) qk(0, base);
-                if (ok && it.jb1 > it.ja) qk(1, base);
-            }
-#pragma unroll 1
-            for (int turn = 0; ok && turn < 2 * (it.jb - it.ja); ++turn) {
-                const int i = turn & 1, j = turn >> 1, left = (i ? it.jb1 : it.jb0) - it.ja - j;
-                if (left <= 0) continue;
-                const uint32_t n = base + 2 * j + 1, tile = (i ? tiles1 : tiles0) + j;
-                const uint64_t vd = vd0 + uint32_t((n % ST) * P::kTile >> 4);
-#pragma unroll
-                for (int h = 0; h < kParts; ++h) {
-                    ok = ok && spin_wait(smem_u32(&bars.p[i][h]), tile & 1, abort);
-                    if (!ok) break;
+            if (elect_one()) {
+                if (it.jb > it.ja) {
+                    ok = mbar_wait_spin(smem_u32(&bars.q), worked & 1, abort, a.fault ? 100000 : kWaitCycles) &&
+                         mbar_wait_spin(smem_u32(&bars.full[base % ST]), (base / ST) & 1, abort);
                     tc_fence_after();
-                    if (elect_one()) {
+                    if (ok && it.jb0 > it.ja) qk(0, base);
+                    if (ok && it.jb1 > it.ja) qk(1, base);
+                }
+#pragma unroll 1
+                for (int turn = 0; ok && turn < 2 * (it.jb - it.ja); ++turn) {
+                    const int i = turn & 1, j = turn >> 1, left = (i ? it.jb1 : it.jb0) - it.ja - j;
+                    if (left <= 0) continue;
+                    const uint32_t n = base + 2 * j + 1, tile = (i ? tiles1 : tiles0) + j;
+                    const uint64_t vd = vd0 + uint32_t((n % ST) * P::kTile >> 4);
+                    if (kOwnP) {
+                        ok = mbar_wait_spin(smem_u32(&bars.l[i]), tile & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (left > 1) qk(i, n + 1);
+                    }
+#pragma unroll
+                    for (int h = 0; h < kParts; ++h) {
+                        ok = ok && mbar_wait_spin(smem_u32(&bars.p[i][h]), tile & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
                         for (int s = h * 8 / kParts; s < (h + 1) * 8 / kParts; ++s)
-                            mma_f16_tmem_a(tmem + 256 + i * DP, tmem + i * kKeys + s * 8,
+                            mma_f16_tmem_a(tmem + 256 + i * DP, tmem + kPCol + i * kPStep + s * 8,
                                            vd + uint32_t(s * 16 * 128 >> 4), a.idesc_pv, j > 0 || s > 0);
                     }
-                    __syncwarp();
+                    if (!ok) break;
+                    if (!kOwnP && left > 1) qk(i, n + 1);
+                    else mma_commit(smem_u32(&bars.o[i]));
                 }
-                if (!ok) break;
-                if (left > 1) qk(i, n + 1);
-                else if (elect_one()) mma_commit(smem_u32(&bars.o[i]));
-                __syncwarp();
             }
+            __syncwarp();
+            ok = !*abort;
             advance(it);
             if (ok) done_with_item(k);
         }
@@ -584,7 +599,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         }
     } else {
         // ------------------------------------------------ gate (warp 10): V_j and K_{j+1} have arrived
-        // One arrival of each half's weight barrier, so that the issuer waits for nothing else, after
+        // One arrival of each half's weight barrier (and of that of loaded scores, where S(j + 1) waits
+        // for it), so that the issuer waits for nothing else, after
         // V rows that not every row sees are cleaned, and the releases of a half that takes no part.
         bool ok = true;
         Item it;
@@ -617,8 +633,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         continue;
                     }
                     const uint32_t tile = (i ? tiles1 : tiles0) + (j - it.ja);
-                    if (tile > 0) ok = warp_wait(smem_u32(&bars.p[i][0]), (tile - 1) & 1, abort);
-                    if (ok && lane == 0) mbar_arrive(smem_u32(&bars.p[i][0]));
+                    auto add = [&](uint64_t &bar) {  // to this tile's phase: the last tile's is complete
+                        if (tile > 0) ok = ok && warp_wait(smem_u32(&bar), (tile - 1) & 1, abort);
+                        if (ok && lane == 0) mbar_arrive(smem_u32(&bar));
+                    };
+                    if (kOwnP) add(bars.l[i]);
+                    add(bars.p[i][0]);
                 }
                 __syncwarp();
             }
@@ -635,6 +655,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         const int i = warp >> 2;
         const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 256 + i * DP;
+        const uint32_t p_addr = tmem + lanes + kPCol + i * kPStep;
         const bool releases = (tid & 127) == 0;
         const int mine = (tid & 127) / a.group;  // this row's token within the half
         uint32_t tiles = 0, outputs = 0;  // tiles of this half so far, items in which it took part
@@ -658,18 +679,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             for (int j = 0; j < count; ++j) {
                 ok = warp_wait(smem_u32(&bars.s[i]), (tiles + j) & 1, abort);
                 if (!ok) break;
-                if (releases) {  // S_i(j) is complete: so are O_i's product with V_{j-1} and the reads of K_j
-                    const uint32_t n = base + 2 * j;
-                    mbar_arrive(smem_u32(&bars.empty[n % ST]));
-                    if (j > 0) mbar_arrive(smem_u32(&bars.empty[(n - 1) % ST]));
-                    if (j + 1 == count) mbar_arrive(smem_u32(&bars.q_empty));
-                }
+                // S_i(j) is complete: so are the reads of K_j and, unless it was issued before it, O_i's
+                // product with V_{j-1}
+                auto release = [&](uint32_t n) {
+                    if (releases) mbar_arrive(smem_u32(&bars.empty[n % ST]));
+                };
+                release(base + 2 * j);
+                if (!kOwnP && j > 0) release(base + 2 * j - 1);
+                if (releases && j + 1 == count) mbar_arrive(smem_u32(&bars.q_empty));
                 tc_fence_after();
                 float s[kKeys];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_addr + c * 32, *reinterpret_cast<float(*)[32]>(s + c * 32));
                 tmem_ld_wait();
                 loaded(s);
+                if (kOwnP) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars.l[i]));
+                }
                 if ((j + 1) * kKeys > vis_half) {
                     const int left = vis - j * kKeys;
 #pragma unroll
@@ -687,6 +715,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     }
                 }
                 const float most = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+                if (kOwnP && j > 0) {  // the last weights are read and O_i is at rest
+                    ok = warp_wait(smem_u32(&bars.o[i]), (tiles + j - 1) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    release(base + 2 * j - 1);
+                }
                 // move the maximum when a score passes it by more than the slack
                 const bool move = (most - top) * a.scale_log2 > kSlack || (top == -INFINITY && most > -INFINITY);
                 if (j == 0) {
@@ -697,7 +731,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     top = now;
                     sum0 *= f;
                     sum1 *= f;
-                    // S_i(j) was issued after O_i's last product, so that one is done
+                    // O_i's last product is done: awaited, or issued before S_i(j)
 #pragma unroll 1
                     for (int c = 0; c < DP / 16; ++c) {
                         float o[16];
@@ -722,7 +756,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         p[e] = pack2<T>(s[x], s[x + 1]);
                         add2(sum0, sum1, s[x], s[x + 1]);
                     }
-                    tmem_st_32x32b_x16(s_addr + c * 16, p);
+                    tmem_st_32x32b_x16(p_addr + c * 16, p);
                     if (c % (4 / kParts) == 4 / kParts - 1) {  // a part of the keys: its product may begin
                         tmem_st_wait();
                         tc_fence_before();
@@ -732,7 +766,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 }
             }
             if (ok && count > 0) {
-                ok = warp_wait(smem_u32(&bars.o[i]), outputs & 1, abort);
+                ok = warp_wait(smem_u32(&bars.o[i]), (kOwnP ? tiles + count - 1 : outputs) & 1, abort);
                 ++outputs;
                 if (ok && releases) mbar_arrive(smem_u32(&bars.empty[(base + 2 * count - 1) % ST]));
             }
@@ -893,6 +927,7 @@ TcArgs common_args(const HeadShape &shape, qmm_float t, float scale, void *ws) {
     a.idesc_qk = idesc_f16_f32(kRows, kKeys) | type_bits | (scale < 0.f ? 1u << 13 : 0u);
     a.idesc_pv = idesc_f16_f32(kRows, shape.d <= 64 ? 64 : 128) | type_bits | (1u << 16);
     a.status = static_cast<int *>(ws);
+    a.fault = test_fault_mode();
     return a;
 }
 

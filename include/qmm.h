@@ -523,7 +523,8 @@ QMM_API void qmm_set_stream_k_mode(int mode);
  * out (after about 10^5 cycles instead of about a second): the kernel stops, frees
  * its tensor memory and sets QMM_ERR_DEVICE in the workspace's status word, which
  * qmm_read_device_status / qmm_get_device_status return.  No copy is in flight when
- * the kernel leaves and the context stays usable; y is unspecified for that call. */
+ * the kernel leaves and the context stays usable; y is unspecified for that call.  The
+ * attention calls issue no copy at all while it is set, and report the same way. */
 QMM_API void qmm_set_test_fault(int mode);
 
 #ifdef __cplusplus
