@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 for (int e = 0; e < kUnits; ++e)
                     to[e] = __shfl_sync(0xffffffffu, out_row, (32 / kUnits) * e + (lane & (32 / kUnits - 1)));
 #pragma unroll 1
-                for (int c = 0; c < DP; c += 32) {  // rolled: code that runs once an item is fetched anew each time
+                for (int c = 0; c < DP && __any_sync(0xffffffffu, row_valid); c += 32) {  // rolled: code that runs once an item is fetched anew each time
                     float o[32];
                     tmem_ld_32x32b_x32(o_addr + c, o);
                     tmem_ld_wait();

@@ -48,6 +48,30 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 v) {
         make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
+// Eight elements: x at p + e0 and y at p + e1, one access when they are neighbours and 16 bits wide.
+template <bool kNext, typename In> __device__ __forceinline__ void load8(const In *p, int e0, int e1, float4 &x, float4 &y) {
+    if constexpr (kNext && sizeof(In) == 2) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p + e0);
+        const uint2 h[2] = {make_uint2(u.x, u.y), make_uint2(u.z, u.w)};
+        x = load4(reinterpret_cast<const In *>(&h[0]));
+        y = load4(reinterpret_cast<const In *>(&h[1]));
+    } else {
+        x = load4(p + e0);
+        y = load4(p + e1);
+    }
+}
+template <bool kNext, typename Out> __device__ __forceinline__ void store8(Out *p, int e0, int e1, float4 x, float4 y) {
+    if constexpr (kNext) {
+        uint2 h[2];
+        store4(reinterpret_cast<Out *>(&h[0]), x);
+        store4(reinterpret_cast<Out *>(&h[1]), y);
+        *reinterpret_cast<uint4 *>(p + e0) = make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+    } else {
+        store4(p + e0, x);
+        store4(p + e1, y);
+    }
+}
+
 // Sine and cosine of pos * freq.  The angle is taken in turns as a 64-bit fraction, whose whole
 // turns fall off by themselves: freq / (2 pi) = m 2^q / (2 pi) for freq's mantissa m, with 1 / (2 pi)
 // as a 64-bit integer over 2^66, times pos modulo 2^64.  Exact to 2^-32 of a turn at every int32 position.
@@ -70,7 +94,7 @@ __device__ __forceinline__ float2 cos_sin(int pos, float freq) {
     return make_float2(c, s);
 }
 
-template <typename In, typename Out>
+template <typename In, typename Out, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a, int lanes_log2, int share) {
     __shared__ float2 cs[kMaxHeadDim / 2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -83,7 +107,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
     const int h_begin = blockIdx.y * share, h_end = min(total, h_begin + share);
     const bool live = 8 * c < d, turned = 8 * c < r;
     // this lane's elements e0..e0+3 and e1..e1+3: pairs across them, or within each when interleaved
-    const int e0 = turned && !a.interleaved ? 4 * c : 8 * c, e1 = turned && !a.interleaved ? r / 2 + 4 * c : 8 * c + 4;
+    const int e0 = turned && !kInterleaved ? 4 * c : 8 * c, e1 = turned && !kInterleaved ? r / 2 + 4 * c : 8 * c + 4;
 
     auto load = [&](int h, float4 &x, float4 &y) {
         x = y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -91,8 +115,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
         const In *p = h < hq        ? static_cast<const In *>(a.q) + t * a.sq.t + h * a.sq.h
                       : h < hq + hk ? static_cast<const In *>(a.k) + t * a.sk.t + (h - hq) * a.sk.h
                                     : static_cast<const In *>(a.v) + t * a.sv.t + (h - hq - hk) * a.sv.h;
-        x = load4(p + e0);
-        y = load4(p + e1);
+        load8<kInterleaved>(p, e0, e1, x, y);
     };
     int h = h_begin + warp * per_warp + sub;
     const int step = kRopeWarps * per_warp;
@@ -124,7 +147,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
                 q = q * cs.x + p * cs.y;
                 p = n;
             };
-            if (a.interleaved) {
+            if (kInterleaved) {
                 rotate(A.x, A.y, turn[0]);
                 rotate(A.z, A.w, turn[1]);
                 rotate(B.x, B.y, turn[2]);
@@ -139,8 +162,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
         Out *out = is_q    ? static_cast<Out *>(a.qo) + t * a.sqo.t + h * a.sqo.h
                    : !is_v ? static_cast<Out *>(a.ko) + t * a.sko.t + (h - hq) * a.sko.h
                            : static_cast<Out *>(a.vo) + t * a.svo.t + (h - hq - hk) * a.svo.h;
-        store4(out + e0, A);
-        store4(out + e1, B);
+        store8<kInterleaved>(out, e0, e1, A, B);
     }
 }
 
@@ -152,7 +174,8 @@ template <typename In, typename Out> cudaError_t launch_typed(const RopeArgs &a,
     const int round = kRopeWarps * (32 >> lanes_log2);
     const int share = a.m < 4 * device_sm_count() ? round : (total + round - 1) / round * round;
     const dim3 grid((unsigned)a.m, (unsigned)((total + share - 1) / share));
-    qk_norm_rope_kernel<In, Out><<<grid, kRopeThreads, 0, st>>>(a, lanes_log2, share);
+    auto kern = a.interleaved ? qk_norm_rope_kernel<In, Out, true> : qk_norm_rope_kernel<In, Out, false>;
+    kern<<<grid, kRopeThreads, 0, st>>>(a, lanes_log2, share);
     return cudaGetLastError();
 }
 
