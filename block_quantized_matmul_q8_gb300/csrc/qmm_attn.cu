@@ -10,6 +10,11 @@
 // The partial rows stay in shared memory and are joined through the cluster: no second launch
 // and no workspace.  The products run on mma.sync: with 16 rows the copies take an order of
 // magnitude longer than the tensor work, and tcgen05's 128 rows would stay empty.
+//
+// 48 caches of up to 8192 rows, 32/8 heads of 128: 129 us, 6.35 TB/s (95% of the measured copy
+// rate).  One request of 640 rows: 6 us, of which a tile's copy, products and join take 4 and the
+// launch 2.  64 requests of up to 512 rows after a prefix of 8192: 35 us, the tensor-core phase and
+// the caches after one another on most SMs, 4 to 5 us of it starts and joins.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -12,7 +12,7 @@ using namespace qmm;
 
 namespace {
 
-constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1024;  // a tile past the last token still counts in 32 bits
 constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kMaxSeqs = int64_t(1) << 20;
 constexpr int64_t kMaxGroup = 128;  // query heads of one key/value head
