@@ -4,7 +4,8 @@
  * The library computes y[m][n] = sum_k x[m][k] * dequant(W)[n][k] with W kept in
  * its block-quantized form (Q4_K, Q5_K, Q6_K, Q8_0 or Q4_0) and x quantized to q8_1 first.
  * Every product is formed from exact integer sub-block dot products that are
- * then folded with the block scales in fp32.
+ * then folded with the block scales in fp32.  Between two such projections stand the
+ * attention calls: norm and rotation of heads, packed prompts, decoding batches.
  *
  * Sources (web pages on block-quantized matmul), cited by title and section:
  *   [MMQ]   "llama.cpp 源码完全拆解(十五): 量化 GEMM 的矩阵编队 -- MMQ 如何把 MoE 与预填充塞满 GPU"
@@ -420,6 +421,10 @@ QMM_API qmm_status qmm_qk_norm_rope(const qmm_heads *q, const qmm_heads *k, cons
  * influence on it, whatever its k and v hold (infinities and NaN included).  Query rows
  * outside every sequence are not written.  heads_q is a multiple of heads_kv, at most 128
  * times it; head_dim a multiple of 8, 8..128.
+ * The same inputs on the same GPU give the same bits.  Accuracy, with u = 2^-8 (bf16) or 2^-11
+ * (f16): |out - exact| <= u |out| + (u + e) sum_j p_j |v_j|, where e <= 2^-18 head_dim scale
+ * max_j sum_d |q_d k_jd| + 2^-16 covers the fp32 scores, exponentials and sums; in f16 a weight
+ * below 2^-14 of the largest is off by up to 2^-25 of it.
  */
 QMM_API size_t qmm_workspace_bytes_attn_prompt(int64_t tokens_q, int64_t tokens_k, int64_t n_seqs, int64_t heads_q,
                                                int64_t heads_kv, int64_t head_dim);
