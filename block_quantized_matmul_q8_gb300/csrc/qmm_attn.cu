@@ -39,9 +39,11 @@ constexpr int kMaxCluster = 16;
 template <int DP> struct Ring {
     // Stages hold a K tile or a V tile by turns: DP/64 blocks of 64 x 128 bytes.  64 KB of them and
     // 128 registers a thread let three CTAs share an SM, so that one's start and join overlap the
-    // others' copies.
+    // others' copies; heads up to 64 take 48 KB and 96 registers, and four (35 requests of 16 heads
+    // on a prefix of 297: 13.5 -> 9.1 us; with 128-element heads four take 133 us where three take 129).
     static constexpr int kTile = kTileKeys * DP * 2;
-    static constexpr int kStages = DP == 128 ? 4 : 8;
+    static constexpr int kStages = DP == 128 ? 4 : 6;
+    static constexpr int kCtas = DP == 128 ? 3 : 4;   // of one SM
     static constexpr int kPartStride = DP + 4;        // floats between a warp's partial rows
     static constexpr size_t kBytes = size_t(kStages) * kTile + 1024;
     static constexpr int kParts = kWarps * kMaxRows * kPartStride;  // floats of the CTA's partial rows
@@ -132,7 +134,7 @@ __device__ __forceinline__ float4 peer_f32x4(uint32_t addr, uint32_t rank) {
 // Byte of 16-byte unit u of a row in a block of rows of 128 bytes, 128-byte swizzled.
 __device__ __forceinline__ uint32_t swizzled(int row, int u) { return uint32_t(row * 128 + ((u ^ (row & 7)) << 4)); }
 
-template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 3) attn_decode_kernel(const __grid_constant__ DecArgs a) {
+template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<DP>::kCtas) attn_decode_kernel(const __grid_constant__ DecArgs a) {
     using R = Ring<DP>;
     constexpr int ST = R::kStages, KS = DP / 16;
     extern __shared__ uint8_t raw[];
@@ -225,7 +227,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, 3) att
                 }
         }
         for (int i = 0; i < n; ++i) {
-            const int k_stg = (2 * i) % ST, v_stg = k_stg + 1, phase = ((2 * i) / ST) & 1;
+            const int k_stg = (2 * i) % ST, v_stg = k_stg + 1, phase = ((2 * i) / ST) & 1;  // ST is even
             const uint32_t kt = sm + k_stg * R::kTile, vt = kt + R::kTile;
             if (!warp_wait(smem_u32(&full[k_stg]), phase, abort, a.fault ? 100000 : kWaitCycles)) break;
             const int64_t j = j0 + i;
@@ -441,14 +443,15 @@ bool prefix_on_tensor_cores(const DecodeArgs &d) {
 }
 
 // CTAs of one request and kv head (a power of two, at most one for each key tile): as many as
-// leave every CTA resident at once with room to spare (two an SM: a grid of clusters that nearly
-// fills the SMs runs its last clusters on their own; 112 pairs of 19 tiles: 9.8 us with 2 CTAs
-// each, 13.3 with 4), or, for long caches, parts of at least 32 tiles, which level out ragged
+// leave every CTA resident at once with room to spare (one an SM fewer than fit: a grid of clusters
+// that nearly fills the SMs runs its last clusters on their own; 112 pairs of 19 tiles with three
+// CTAs an SM: 9.8 us with 2 CTAs each, 13.3 with 4), or, for long caches, parts of at least 32 tiles, which level out ragged
 // lengths (48 x 8 pairs of up to 128 tiles: 140 us with 1, 129 with 4).
 int cluster_ctas(const DecodeArgs &d, int64_t inline_prefix, int64_t pairs) {
     const int64_t tiles = (inline_prefix + kTileKeys - 1) / kTileKeys + (d.room + kTileKeys - 1) / kTileKeys;
+    const int64_t room = int64_t(d.shape.d <= 64 ? Ring<64>::kCtas - 1 : Ring<128>::kCtas - 1) * device_sm_count();
     int c = 1;
-    while (c < kMaxCluster && tiles >= 2 * c && (pairs * 2 * c <= 2 * device_sm_count() || tiles >= 64 * c)) c *= 2;
+    while (c < kMaxCluster && tiles >= 2 * c && (pairs * 2 * c <= room || tiles >= 64 * c)) c *= 2;
     return c;
 }
 
