@@ -503,7 +503,7 @@ def _scratch(need, workspace, like):
         _dev(workspace, "workspace")
         return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size(), False
     if need > 256:
-        workspace = like.new_empty(need, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
         return workspace, workspace.data_ptr(), need, True
     device = like.get_device()
     block = _status_words.get(device)
@@ -624,9 +624,8 @@ def qmm_attn_decode(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | N
     b, hq, d = shape
     if dtype not in FLOATS:
         raise QMMError(3, "q must be fp16 or bf16")
-    for pair, what in (((k, v), "k and v"), ((prefix_k, prefix_v), "prefix_k and prefix_v")):
-        if (pair[0] is None) != (pair[1] is None):
-            raise QMMError(1, f"{what} go together")
+    if (k is None) != (v is None) or (prefix_k is None) != (prefix_v is None):
+        raise QMMError(1, "k and v, and prefix_k and prefix_v, go together")
     room = p = kb = vb = 0
     kh = vh = pk = pv = _NO_VIEW
     if k is not None:

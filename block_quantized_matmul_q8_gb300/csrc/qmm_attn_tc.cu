@@ -808,19 +808,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                     loaded(o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
-                    if (odd && row_valid) {  // non-finite values that were taken out of V
-                        const int from = max(it.vis_lo, it.ja * kKeys);
-                        const int end = min(visible(a, it, t), (it.ja + count) * kKeys);
-                        const T *v = static_cast<const T *>(a.v_data) + it.hk * a.sv.h + c;
-#pragma unroll 1
-                        for (int key = from; key < end; ++key)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                if (c + e >= a.shape.d) continue;
-                                const float x = float(v[(int64_t(it.k0) + key) * a.sv.t + e]);
-                                if (!isfinite(x)) o[e] += x;
-                            }
-                    }
                     uint4 x[kUnits];
 #pragma unroll
                     for (int e = 0; e < kUnits; ++e) {
@@ -836,6 +823,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < kUnits; ++e)
                         if (to[e] >= 0 && col < a.shape.d) *reinterpret_cast<uint4 *>(out + to[e] + col) = x[e];
+                }
+                if (odd) {
+                    // Non-finite values that were taken out of V: an element of a row that sees one is
+                    // their sum, whatever the finite ones come to.  After the warp's stores above.
+                    __syncwarp();
+                    const int from = max(it.vis_lo, it.ja * kKeys);
+                    const int end = row_valid ? min(visible(a, it, t), (it.ja + count) * kKeys) : from;
+                    const T *v = static_cast<const T *>(a.v_data) + it.hk * a.sv.h;
+#pragma unroll 1
+                    for (int e = 0; e < a.shape.d; ++e) {
+                        float total = 0.f;
+#pragma unroll 1
+                        for (int key = from; key < end; ++key) {
+                            const float x = float(v[(int64_t(it.k0) + key) * a.sv.t + e]);
+                            if (!isfinite(x)) total += x;
+                        }
+                        if (!isfinite(total)) out[out_row + e] = Out(total);
+                    }
                 }
                 if (row_valid) {
                     const float l2 = none ? -INFINITY : top * a.scale_log2 + log2f(sum);
