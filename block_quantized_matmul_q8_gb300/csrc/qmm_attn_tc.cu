@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     // the weights take the place of their scores, so that S(j + 1) waits for the product with V_j.  With
     // DP = 64 they have columns of their own: S(j + 1) is formed as soon as the softmax has loaded S(j),
     // and the softmax is never without scores (5 prompt chunks of up to 509 tokens after 3500, 32 heads
-    // of 64: 47.6 -> 36 us).
+    // of 64: 47.6 -> 42 us).
     constexpr bool kOwnP = DP == 64;
     constexpr int kPCol = kOwnP ? 256 + 2 * DP : 0, kPStep = kOwnP ? kKeys / 2 : kKeys;
     constexpr int kParts = kOwnP ? 1 : 2;  // parts of a tile's weights that are handed over one by one

@@ -415,8 +415,9 @@ QMM_API qmm_status qmm_qk_norm_rope(const qmm_heads *q, const qmm_heads *k, cons
  *                lq queries and lk keys sees the keys j <= i + (lk - lq).
  *   q, out     : type t [tokens_q] tokens of heads_q heads; k, v: [tokens_k] tokens of heads_kv.
  *   lse        : fp32 [tokens_q][heads_q], the log of the softmax's denominator, or NULL.
- *   workspace  : qmm_workspace_bytes_attn_prompt(...) bytes, 256-byte aligned; it also holds
- *                the status word of qmm_read_device_status.
+ *   workspace  : qmm_workspace_bytes_attn_prompt(...) bytes (for the current device: the parts
+ *                of split keys depend on its SMs), 256-byte aligned; it also holds the status
+ *                word of qmm_read_device_status.
  * A row that sees no key gives zeros (lse -infinity).  A key that a row does not see has no
  * influence on it, whatever its k and v hold (infinities and NaN included).  Query rows
  * outside every sequence are not written.  heads_q is a multiple of heads_kv, at most 128
@@ -445,8 +446,8 @@ QMM_API qmm_status qmm_attn_prompt(const qmm_heads *q, const qmm_heads *k, const
  *   prefix_k, prefix_v : [prefix_len] tokens of heads_kv heads; prefix_len == 0: none (may be
  *            NULL), which is the single-token form of attention over separate caches.
  *   room may be 0 (then k, v may be NULL).  lse: fp32 [batch][heads_q] or NULL.
- *   workspace : qmm_workspace_bytes_attn_decode(...) bytes, 256-byte aligned; it also holds the
- *            status word of qmm_read_device_status.
+ *   workspace : qmm_workspace_bytes_attn_decode(...) bytes (for the current device), 256-byte
+ *            aligned; it also holds the status word of qmm_read_device_status.
  * Cache rows from lens[b] on have no influence, whatever they hold.  A request without any
  * key gives zeros (lse -infinity).  Heads and sizes as for qmm_attn_prompt.
  */
