@@ -825,8 +825,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                         if (to[e] >= 0 && col < a.shape.d) *reinterpret_cast<uint4 *>(out + to[e] + col) = x[e];
                 }
                 if (odd) {
-                    // Non-finite values that were taken out of V: an element of a row that sees one is
-                    // their sum, whatever the finite ones come to.  After the warp's stores above.
+                    // Non-finite values that were taken out of V: a row that sees one adds it to what the
+                    // rest came to, which may be an infinity or NaN itself (a NaN score, a value of a tile
+                    // that every row sees).  After the warp's stores above, which other lanes made.
                     __syncwarp();
                     const int from = max(it.vis_lo, it.ja * kKeys);
                     const int end = row_valid ? min(visible(a, it, t), (it.ja + count) * kKeys) : from;
@@ -839,7 +840,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                             const float x = float(v[(int64_t(it.k0) + key) * a.sv.t + e]);
                             if (!isfinite(x)) total += x;
                         }
-                        if (!isfinite(total)) out[out_row + e] = Out(total);
+                        if (!isfinite(total)) out[out_row + e] = Out(float(out[out_row + e]) + total);
                     }
                 }
                 if (row_valid) {
