@@ -341,6 +341,7 @@ template <typename T, int DP> __device__ __forceinline__ bool clean_values(uint8
         }
     }
     fence_proxy_async_smem();
+    __syncwarp();  // one lane arrives for all: the others' rows come first
     return odd;
 }
 
