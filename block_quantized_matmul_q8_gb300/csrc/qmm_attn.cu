@@ -59,7 +59,8 @@ struct DecArgs {
     int parts;               // partial rows of the tensor-core phase to join
     const float *part, *part_lse;
     float scale_log2;
-    int fault;               // qmm_set_test_fault: no copy is issued, and the waits for them are short
+    int fault;               // qmm_set_test_fault: 1 no copy is issued, and the waits for them are short;
+                             // 2 the copies are issued, and the first wait for one gives up at once
     int *status;
 };
 
@@ -139,7 +140,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<D
     constexpr int ST = R::kStages, KS = DP / 16;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[ST], empty[ST];
-    __shared__ int abort_s;
+    __shared__ int abort_s, issued_s;  // issued: copies so far
     __shared__ float ml_s[kWarps][kMaxRows][2];  // each warp's maximum and sum (log2 domain)
     __shared__ float joined_s[kMaxRows][2];      // the CTA's
     const DecodeArgs &d = a.d;
@@ -161,7 +162,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<D
 
     const uint32_t sm = (smem_u32(raw) + 1023u) & ~1023u;
     if (tid == 0) {
-        abort_s = 0;
+        abort_s = issued_s = 0;
         for (int i = 0; i < ST; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&empty[i]), kWarps);
@@ -182,9 +183,8 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<D
     if (warp == kWarps) {
         // ------------------------------------------------ copies
         bool ok = true;
-        int issued = 0;
         if (lane == 0) {
-            for (int i = 0; i < 2 * n && ok && !a.fault; ++i) {
+            for (int i = 0; i < 2 * n && ok && a.fault != 1; ++i) {
                 const int stg = i % ST, kv = i & 1;
                 if (i >= ST) ok = mbar_wait(smem_u32(&empty[stg]), ((i / ST) - 1) & 1, abort);
                 if (!ok) break;
@@ -197,13 +197,8 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<D
                     if (j < ptiles) tma_load_3d(to, kv ? &a.pv : &a.pk, c * 64, hk, int(j * kTileKeys), bar);
                     else tma_load_4d(to, kv ? &a.v : &a.k, c * 64, hk, int((j - ptiles) * kTileKeys), int(b), bar);
                 }
-                issued = i + 1;
+                issued_s = i + 1;
             }
-            if (!ok)  // a wait gave up: the copies in flight land before the ring is reused or released
-                for (int i = max(issued - ST, 0); i < issued; ++i) {
-                    int never = 0;
-                    mbar_wait(smem_u32(&full[i % ST]), (i / ST) & 1, &never);
-                }
         }
         __syncwarp();
     }
@@ -229,7 +224,8 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<D
         for (int i = 0; i < n; ++i) {
             const int k_stg = (2 * i) % ST, v_stg = k_stg + 1, phase = ((2 * i) / ST) & 1;  // ST is even
             const uint32_t kt = sm + k_stg * R::kTile, vt = kt + R::kTile;
-            if (!warp_wait(smem_u32(&full[k_stg]), phase, abort, a.fault ? 100000 : kWaitCycles)) break;
+            if (a.fault == 2) *abort = 1;
+            if (a.fault == 2 || !warp_wait(smem_u32(&full[k_stg]), phase, abort, a.fault ? 100000 : kWaitCycles)) break;
             const int64_t j = j0 + i;
             const int64_t left = j < ptiles ? a.inline_prefix - j * kTileKeys : len - (j - ptiles) * kTileKeys;
             const int valid = int(min(left, int64_t(kTileKeys))) - warp * 16;  // of this warp's keys
@@ -314,7 +310,15 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<D
             sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
         }
     }
-    __syncthreads();  // the ring is free: every copy was waited for
+    __syncthreads();  // the ring is free: every copy was waited for,
+    if (*abort) {     // or a wait gave up, and the copies in flight land before the ring is reused or released
+        if (tid == kWarps * 32)
+            for (int i = max(issued_s - ST, 0); i < issued_s; ++i) {
+                int never = 0;
+                mbar_wait(smem_u32(&full[i % ST]), (i / ST) & 1, &never);
+            }
+        __syncthreads();
+    }
     float *part = reinterpret_cast<float *>(raw + (sm - smem_u32(raw)));
     // weights of the partial rows in the join: the cluster's CTAs and the tensor-core phase's splits
     auto weight_s = reinterpret_cast<float(*)[kMaxCluster + 1]>(part + R::kParts);

@@ -73,7 +73,8 @@ struct TcArgs {
     int causal, splits;
     float scale_log2;       // |scale| * log2(e)
     uint32_t idesc_qk, idesc_pv;
-    int fault;              // qmm_set_test_fault: no copy is issued, and the first wait for one is short
+    int fault;              // qmm_set_test_fault: 1 no copy is issued, and the first wait for one is short;
+                            // 2 the copies are issued, and the first wait for one gives up at once
     int *status;
 };
 
@@ -402,11 +403,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     __shared__ __align__(16) uint4 answer;
     __shared__ uint32_t tmem_s;
     __shared__ int abort_s;
+    __shared__ uint32_t issued_s, q_issued_s;  // ring copies and items' Q copies so far
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     grid_launch_dependents();  // a launch that waits for this one's end may take free SMs
 
     if (tid == 0) {
         abort_s = 0;
+        issued_s = q_issued_s = 0;
         for (int i = 0; i < ST; ++i) {
             mbar_init(smem_u32(&bars.full[i]), 1);
             mbar_init(smem_u32(&bars.empty[i]), 2);
@@ -493,7 +496,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     } else if (warp == 8) {
         // ------------------------------------------------ copies
         bool ok = true;
-        uint32_t issued = 0, q_issued = 0;
         if (lane == 0) {
             prefetch_tmap(&a.q);
             prefetch_tmap(&a.k);
@@ -503,8 +505,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (int k = 0; get_item(k, it); ++k) {
             if (it.jb > it.ja) {
                 if (worked > 0) ok = warp_wait(smem_u32(&bars.q_empty), (worked - 1) & 1, abort);
-                if (ok && !a.fault) ++q_issued;
-                if (ok && lane == 0 && !a.fault) {
+                if (ok && lane == 0 && a.fault != 1) {
                     const uint32_t bar = smem_u32(&bars.q), box = uint32_t(a.group * a.per_half) * 128;
                     const bool half[2] = {it.jb0 > it.ja, it.jb1 > it.ja};
                     mbar_arrive_expect_tx(bar, box * (DP / 64) * (uint32_t(half[0]) + uint32_t(half[1])));
@@ -513,6 +514,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                             if (half[i])
                                 tma_load_3d(sq + i * P::kTile + b * kRows * 128, &a.q, b * 64, it.hk * a.group,
                                             it.q0 + it.t0 + i * a.per_half, bar);
+                    q_issued_s = worked + 1;
                 }
                 __syncwarp();
             }
@@ -520,14 +522,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     const uint32_t n = base + 2 * (j - it.ja) + kv, stg = n % ST;
                     if (n >= ST) ok = warp_wait(smem_u32(&bars.empty[stg]), (n / ST - 1) & 1, abort);
-                    if (ok && lane == 0 && !a.fault) {
+                    if (ok && lane == 0 && a.fault != 1) {
                         const uint32_t bar = smem_u32(&bars.full[stg]);
                         mbar_arrive_expect_tx(bar, P::kTile);
                         for (int b = 0; b < DP / 64; ++b)
                             tma_load_3d(skv + stg * P::kTile + b * kKeys * 128, kv ? &a.v : &a.k, b * 64, it.hk,
                                         it.k0 + j * kKeys, bar);
+                        issued_s = n + 1;
                     }
-                    if (ok && !a.fault) issued = n + 1;
                     __syncwarp();
                 }
             }
@@ -535,14 +537,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             advance(it);
             if (!ok) break;
             done_with_item(k);
-        }
-        if (*abort) {  // a wait gave up: the copies in flight land before shared memory is released
-            int never = 0;
-            if (q_issued > 0) warp_wait(smem_u32(&bars.q), (q_issued - 1) & 1, &never);
-            for (uint32_t n = issued > ST ? issued - ST : 0; n < issued; ++n) {
-                never = 0;
-                warp_wait(smem_u32(&bars.full[n % ST]), (n / ST) & 1, &never);
-            }
         }
     } else if (warp == 9) {
         // ------------------------------------------------ products, issued by one elected lane
@@ -563,7 +557,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
         for (int k = 0; ok && get_item(k, it); ++k) {
             if (elect_one()) {
                 if (it.jb > it.ja) {
-                    ok = mbar_wait_spin(smem_u32(&bars.q), worked & 1, abort, a.fault ? 100000 : kWaitCycles) &&
+                    if (a.fault == 2) *abort = 1;
+                    ok = a.fault != 2 && mbar_wait_spin(smem_u32(&bars.q), worked & 1, abort, a.fault ? 100000 : kWaitCycles) &&
                          mbar_wait_spin(smem_u32(&bars.full[base % ST]), (base / ST) & 1, abort);
                     tc_fence_after();
                     if (ok && it.jb0 > it.ja) qk(0, base);
@@ -600,11 +595,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             ok = !*abort;
             advance(it);
             if (ok) done_with_item(k);
-        }
-        if (*abort) {  // let what was issued end before the tensor memory is freed
-            if (elect_one()) mma_commit(smem_u32(&bars.drain));
-            int never = 0;
-            spin_wait(smem_u32(&bars.drain), 0, &never);
         }
     } else {
         // ------------------------------------------------ gate (warp 10): V_j and K_{j+1} have arrived
@@ -859,7 +849,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (*abort && tid == 0) *a.status = QMM_ERR_DEVICE;
+    if (*abort) {  // a wait gave up: what was issued ends before shared and tensor memory are released
+        int never = 0;
+        if (warp == 8) {
+            if (q_issued_s > 0) warp_wait(smem_u32(&bars.q), (q_issued_s - 1) & 1, &never);
+            for (uint32_t n = issued_s > ST ? issued_s - ST : 0; n < issued_s; ++n) {
+                never = 0;
+                warp_wait(smem_u32(&bars.full[n % ST]), (n / ST) & 1, &never);
+            }
+        } else if (warp == 9) {
+            if (elect_one()) mma_commit(smem_u32(&bars.drain));
+            spin_wait(smem_u32(&bars.drain), 0, &never);
+        }
+        if (tid == 0) *a.status = QMM_ERR_DEVICE;
+        __syncthreads();
+    }
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 

@@ -530,7 +530,9 @@ QMM_API void qmm_set_stream_k_mode(int mode);
  * its tensor memory and sets QMM_ERR_DEVICE in the workspace's status word, which
  * qmm_read_device_status / qmm_get_device_status return.  No copy is in flight when
  * the kernel leaves and the context stays usable; y is unspecified for that call.  The
- * attention calls issue no copy at all while it is set, and report the same way. */
+ * attention calls issue no copy at all while it is set, and report the same way.
+ * 2 = the attention calls issue their copies, and the first wait for one gives up at once:
+ * the copies in flight land before the kernel leaves.  The other calls run as with 0. */
 QMM_API void qmm_set_test_fault(int mode);
 
 #ifdef __cplusplus
