@@ -11,6 +11,7 @@ no other implementation to fall back to.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 import threading
@@ -497,31 +498,39 @@ _status_words = {}
 
 
 def _scratch(need, workspace, like):
-    """(workspace, pointer, bytes, whether it was made for this call).  Where a call needs no more
-    than its status word and the caller gave no workspace, one block for each device takes it."""
+    """(workspace, pointer, bytes).  Where a call needs no more than its status word and the caller
+    gave no workspace, one block for each device takes it."""
     if workspace is not None:
         _dev(workspace, "workspace")
-        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size(), False
+        return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need > 256:
         workspace = torch.empty(need, dtype=torch.uint8, device=like.device)
-        return workspace, workspace.data_ptr(), need, True
+        return workspace, workspace.data_ptr(), need
     device = like.get_device()
     block = _status_words.get(device)
     if block is None:
         block = _status_words[device] = torch.empty(256, dtype=torch.uint8, device=like.device)
-    return block, block.data_ptr(), 256, False
+    return block, block.data_ptr(), 256
 
 
-def _on_stream(stream, *made):
-    """The stream's handle; tensors that a call made for itself are kept until that stream is done with them."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+def _current():
+    """The handle of the current stream."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _on_stream(stream, call, *given):
+    """call() with `stream` as the current one, so that what it allocates comes from that stream's memory
+    and not from blocks that the caller's stream may still use.  Tensors that it returns and the caller
+    did not give are kept until both streams are done with them."""
+    caller = torch.cuda.current_stream()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+    with torch.cuda.stream(stream):
+        result = call()
+    for t in result if isinstance(result, tuple) else (result,):
+        if t is not None and all(t is not g for g in given):
+            t.record_stream(caller)
+    return result
 
 
 def qmm_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None, positions: torch.Tensor | None,
@@ -533,6 +542,9 @@ def qmm_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None, p
     out_dtype together with v; returns (q_out, k_out, v_out).  inv_freq: fp32 [rotary_dim / 2]
     or None for no rotation.  Views of a fused projection's rows are taken as they are, and
     outputs may be views of a cache."""
+    if stream is not None:
+        return _on_stream(stream, functools.partial(qmm_qk_norm_rope, q, k, v, positions, inv_freq, w_q, w_k, eps,
+                                                    interleaved, out_dtype, q_out, k_out, v_out), q_out, k_out, v_out)
     if q.dim() != 3 or k.dim() != 3:
         raise QMMError(2, "q and k must be [tokens, heads, head_dim]")
     shape, dtype = q.shape, q.dtype
@@ -541,13 +553,12 @@ def qmm_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None, p
     if dtype not in FLOATS or out_dtype not in FLOATS:
         raise QMMError(3, "q must be fp32, fp16 or bf16")
     kv = (m, hk, d)
-    made = [None, None, None]
     if q_out is None:
-        made[0] = q_out = torch.empty_like(q, dtype=out_dtype, memory_format=torch.contiguous_format)
+        q_out = torch.empty_like(q, dtype=out_dtype, memory_format=torch.contiguous_format)
     if k_out is None:
-        made[1] = k_out = torch.empty_like(k, dtype=out_dtype, memory_format=torch.contiguous_format)
+        k_out = torch.empty_like(k, dtype=out_dtype, memory_format=torch.contiguous_format)
     if v is not None and v_out is None:
-        made[2] = v_out = torch.empty_like(v, dtype=out_dtype, memory_format=torch.contiguous_format)
+        v_out = torch.empty_like(v, dtype=out_dtype, memory_format=torch.contiguous_format)
     words, at = _views.words, _views.at
     if v is None:
         _pack4(words, 0, *_view(q, "q", shape, dtype), *_view(k, "k", kv, dtype),
@@ -563,7 +574,7 @@ def qmm_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None, p
                                   _small(w_k, "w_k", torch.float32, d), eps,
                                   _small(positions, "positions", torch.int32, m),
                                   _small(inv_freq, "inv_freq", torch.float32, half), 2 * half, interleaved, qo, ko, vo,
-                                  FLOATS[out_dtype], _on_stream(stream, *made)), "qmm_qk_norm_rope")
+                                  FLOATS[out_dtype], _current()), "qmm_qk_norm_rope")
     return q_out, k_out, v_out
 
 
@@ -578,6 +589,9 @@ def qmm_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Attention over packed sequences: q [tokens_q, heads, d], k and v [tokens_k, kv_heads, d] in fp16
     or bf16, cu_q and cu_k int32 [n_seqs + 1] row bounds (cu_k None: the same as cu_q)."""
+    if stream is not None:
+        return _on_stream(stream, functools.partial(qmm_attn_prompt, q, k, v, cu_q, cu_k, causal, scale, out, lse,
+                                                    workspace), out)
     if q.dim() != 3 or k.dim() != 3:
         raise QMMError(2, "q and k must be [tokens, heads, head_dim]")
     shape, dtype = q.shape, q.dtype
@@ -585,9 +599,8 @@ def qmm_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     tk, hk = k.shape[0], k.shape[1]
     if dtype not in FLOATS:
         raise QMMError(3, "q must be fp16 or bf16")
-    made = None
     if out is None:
-        made = out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     kv = (tk, hk, d)
     _pack4(_views.words, 0, *_view(q, "q", shape, dtype), *_view(k, "k", kv, dtype), *_view(v, "v", kv, dtype),
            *_view(out, "out", shape, dtype))
@@ -596,11 +609,11 @@ def qmm_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     bounds_q = _small(cu_q, "cu_q", torch.int32, n + 1)
     bounds_k = bounds_q if cu_k is None else _small(cu_k, "cu_k", torch.int32, n + 1)
     L = lib()
-    ws, ws_ptr, ws_bytes, ws_made = _scratch(L.qmm_workspace_bytes_attn_prompt(tq, tk, n, hq, hk, d), workspace, q)
+    ws, ws_ptr, ws_bytes = _scratch(L.qmm_workspace_bytes_attn_prompt(tq, tk, n, hq, hk, d), workspace, q)
     _check(L.qmm_attn_prompt(q_, k_, v_, FLOATS[dtype], tq, tk, hq, hk, d, bounds_q, bounds_k, n, causal,
                              d ** -0.5 if scale is None else scale, o_,
                              None if lse is None else _small(lse, "lse", torch.float32, tq * hq), ws_ptr, ws_bytes,
-                             _on_stream(stream, made, ws if ws_made else None)), "qmm_attn_prompt")
+                             _current()), "qmm_attn_prompt")
     return out
 
 
@@ -618,6 +631,9 @@ def qmm_attn_decode(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | N
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """One query token for each request, q [batch, heads, d], over prefix_k and prefix_v [prefix_len, kv_heads, d]
     that all requests share and the caches k and v [batch, room, kv_heads, d] with lens int32 [batch]."""
+    if stream is not None:
+        return _on_stream(stream, functools.partial(qmm_attn_decode, q, k, v, lens, prefix_k, prefix_v, scale, out, lse,
+                                                    workspace), out)
     if q.dim() != 3 or (k is None and prefix_k is None):
         raise QMMError(2, "q must be [batch, heads, head_dim], with caches or a prefix")
     shape, dtype = q.shape, q.dtype
@@ -642,17 +658,16 @@ def qmm_attn_decode(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | N
         if k is None:
             hk = prefix_k.shape[1]
         pk, pv = _view(prefix_k, "prefix_k", (p, hk, d), dtype), _view(prefix_v, "prefix_v", (p, hk, d), dtype)
-    made = None
     if out is None:
-        made = out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     _pack6(_views.words, 0, *_view(q, "q", shape, dtype), *kh, *vh, *pk, *pv, *_view(out, "out", shape, dtype))
     q_, k_, v_, pk_, pv_, o_ = _views.at
     L = lib()
-    ws, ws_ptr, ws_bytes, ws_made = _scratch(L.qmm_workspace_bytes_attn_decode(b, room, p, hq, hk, d), workspace, q)
+    ws, ws_ptr, ws_bytes = _scratch(L.qmm_workspace_bytes_attn_decode(b, room, p, hq, hk, d), workspace, q)
     _check(L.qmm_attn_decode(q_, k_, v_, kb, vb, _small(lens, "lens", torch.int32, b), b, room, pk_, pv_, p,
                              FLOATS[dtype], hq, hk, d, d ** -0.5 if scale is None else scale, o_,
                              None if lse is None else _small(lse, "lse", torch.float32, b * hq), ws_ptr, ws_bytes,
-                             _on_stream(stream, made, ws if ws_made else None)), "qmm_attn_decode")
+                             _current()), "qmm_attn_decode")
     return out
 
 
