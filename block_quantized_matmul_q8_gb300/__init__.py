@@ -37,7 +37,7 @@ EXPORTS = ("qmm_status_string", "qmm_q8_1_bytes", "qmm_row_bytes", "qmm_workspac
            "qmm_get_device_status", "qmm_set_test_fault", "qmm_aligned_row_bytes", "qmm_repack_aligned",
            "qmm_workspace_bytes_aligned", "qmm_mul_mat_aligned", "qmm_workspace_bytes_id_glu", "qmm_mul_mat_id_glu",
            "qmm_qk_norm_rope", "qmm_workspace_bytes_attn_prompt", "qmm_attn_prompt",
-           "qmm_workspace_bytes_attn_decode", "qmm_attn_decode")
+           "qmm_workspace_bytes_attn_decode", "qmm_attn_decode", "qmm_take_attn_error")
 
 
 class QMMError(RuntimeError):
@@ -155,6 +155,8 @@ def lib():
     L.qmm_attn_decode.restype = ctypes.c_int
     L.qmm_attn_decode.argtypes = [HP, HP, HP, I64, I64, P, I64, I64, HP, HP, I64, ctypes.c_int, I64, I64, I64, F32, HP,
                                   P, P, SZ, P]
+    L.qmm_take_attn_error.restype = ctypes.c_int
+    L.qmm_take_attn_error.argtypes = [P, P]
     _lib = L
     return L
 
@@ -588,7 +590,8 @@ def qmm_attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Attention over packed sequences: q [tokens_q, heads, d], k and v [tokens_k, kv_heads, d] in fp16
-    or bf16, cu_q and cu_k int32 [n_seqs + 1] row bounds (cu_k None: the same as cu_q)."""
+    or bf16, cu_q and cu_k int32 [n_seqs + 1] row bounds (cu_k None: the same as cu_q).
+    Without a workspace a device error shows in qmm_take_attn_error alone."""
     if stream is not None:
         return _on_stream(stream, functools.partial(qmm_attn_prompt, q, k, v, cu_q, cu_k, causal, scale, out, lse,
                                                     workspace), out)
@@ -630,7 +633,8 @@ def qmm_attn_decode(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | N
                     scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """One query token for each request, q [batch, heads, d], over prefix_k and prefix_v [prefix_len, kv_heads, d]
-    that all requests share and the caches k and v [batch, room, kv_heads, d] with lens int32 [batch]."""
+    that all requests share and the caches k and v [batch, room, kv_heads, d] with lens int32 [batch].
+    Without a workspace a device error shows in qmm_take_attn_error alone."""
     if stream is not None:
         return _on_stream(stream, functools.partial(qmm_attn_decode, q, k, v, lens, prefix_k, prefix_v, scale, out, lse,
                                                     workspace), out)
@@ -669,6 +673,14 @@ def qmm_attn_decode(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | N
                              None if lse is None else _small(lse, "lse", torch.float32, b * hq), ws_ptr, ws_bytes,
                              _current()), "qmm_attn_decode")
     return out
+
+
+def qmm_take_attn_error(stream=None) -> int:
+    """8 (QMM_ERR_DEVICE) if any attention call on the current device has given up a wait since the last
+    time this was asked, with or without a workspace of the caller's, else 0 (synchronises the stream)."""
+    v = ctypes.c_int32(0)
+    _check(lib().qmm_take_attn_error(ctypes.byref(v), _stream(stream)), "qmm_take_attn_error")
+    return v.value
 
 
 def qmm_tile_efficiency_percent(ntiles: int, nsm: int) -> int:

@@ -367,7 +367,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<D
     }
     if (ranks > 1) cluster_sync();
     else __syncthreads();
-    if (*abort && tid == 0) *a.status = QMM_ERR_DEVICE;
+    if (*abort && tid == 0) *a.status = gave_up = QMM_ERR_DEVICE;
 
     // ------------------------------------------------ the join
     if (a.parts > 0) grid_dependency_wait();
@@ -485,6 +485,8 @@ template <typename T, int DP> cudaError_t launch_dp(const DecArgs &a, int64_t pa
 }
 
 }  // namespace
+
+cudaError_t attn_decode_take_gave_up(bool *yes, cudaStream_t st) { return take_gave_up(yes, st); }
 
 size_t attn_decode_workspace_bytes(const DecodeArgs &d) {
     if (!prefix_on_tensor_cores(d)) return 256;

@@ -26,6 +26,21 @@ template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float 
     else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Set by a kernel of this file that gave up a wait, and only taken back by take_gave_up.
+static __device__ int gave_up;
+
+// Whether the flag was set on the current device; clears it.  Synchronises the stream.
+static inline cudaError_t take_gave_up(bool *yes, cudaStream_t st) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, gave_up, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    *yes = v != 0;
+    if (e != cudaSuccess || !v) return e;
+    v = 0;
+    e = cudaMemcpyToSymbolAsync(gave_up, &v, sizeof(v), 0, cudaMemcpyHostToDevice, st);
+    return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
+}
+
 // mbar_wait by a whole warp: all lanes go on, or all give up.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort,
                                           long long limit = ptx::kWaitCycles) {

@@ -68,6 +68,9 @@ constexpr int kMaxSplits = 64;
 int attn_prefix_splits(const DecodeArgs &a);
 cudaError_t launch_attn_prefix(const DecodeArgs &a, qmm_float t, int splits, float *part, float *part_lse, void *ws,
                                cudaStream_t st);
+// Whether a kernel of the two files has given up a wait on the current device since the last call.
+cudaError_t attn_tc_take_gave_up(bool *yes, cudaStream_t st);
+cudaError_t attn_decode_take_gave_up(bool *yes, cudaStream_t st);
 size_t attn_decode_workspace_bytes(const DecodeArgs &a);
 cudaError_t launch_attn_decode(const DecodeArgs &a, qmm_float t, void *ws, cudaStream_t st);
 

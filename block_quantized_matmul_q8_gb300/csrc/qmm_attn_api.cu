@@ -234,4 +234,13 @@ qmm_status qmm_attn_decode(const qmm_heads *q, const qmm_heads *k, const qmm_hea
     return cuda_status(launch_attn_decode(a, t, workspace, st));
 }
 
+qmm_status qmm_take_attn_error(int32_t *status, void *stream) {
+    if (!status) return QMM_ERR_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    bool prompt = false, decode = false;
+    const cudaError_t e = attn_tc_take_gave_up(&prompt, st), f = attn_decode_take_gave_up(&decode, st);
+    *status = prompt || decode ? QMM_ERR_DEVICE : QMM_OK;
+    return cuda_status(e != cudaSuccess ? e : f);
+}
+
 }  // extern "C"

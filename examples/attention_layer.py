@@ -87,6 +87,8 @@ def main(prefix_tokens=4096, batch=16, room=64, steps=4):
     for i in range(steps):
         token = torch.randn(batch, layer.hidden, generator=g, device="cuda:0")
         y, _, _, lens = timed(f"step {i} of {batch} requests", lambda: layer.step(token, (k, v), caches, lens))
+    if qmm.qmm_take_attn_error():
+        raise RuntimeError("an attention call gave up: its output is unspecified")
     print("finite:", bool(torch.isfinite(y).all()))
 
 

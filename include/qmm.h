@@ -460,6 +460,13 @@ QMM_API qmm_status qmm_attn_decode(const qmm_heads *q, const qmm_heads *k, const
                                    int64_t head_dim, float scale, const qmm_heads *out, float *lse, void *workspace,
                                    size_t ws_bytes, void *stream);
 
+/* Whether any attention call on the current device has given up a bounded wait since the last
+ * qmm_take_attn_error: *status is QMM_ERR_DEVICE (the output of a call between the two is
+ * unspecified) or QMM_OK.  Calls that succeed do not clear it, reading does, so one read
+ * covers all calls of a step, whatever their workspaces.  It synchronises `stream`; a call on
+ * another stream is covered once it has run.  Returns QMM_ERR_CUDA if the read fails. */
+QMM_API qmm_status qmm_take_attn_error(int32_t *status, void *stream);
+
 /* ------------------------------------------------------------------ host-side planning
  * These functions run on the host only and never touch a GPU. */
 
