@@ -207,7 +207,9 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<D
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, o[DP / 8][4];
 #pragma unroll
     for (int c = 0; c < DP / 8; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
-    if (warp < kWarps && n > 0) {
+    if (a.fault == 2) {
+        if (n > 0) *abort = 1;
+    } else if (warp < kWarps && n > 0) {
         uint32_t q[KS][4];
         {
             const T *src = static_cast<const T *>(d.q) + b * d.sq.t + head0 * d.sq.h;
@@ -224,8 +226,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(kThreads, Ring<D
         for (int i = 0; i < n; ++i) {
             const int k_stg = (2 * i) % ST, v_stg = k_stg + 1, phase = ((2 * i) / ST) & 1;  // ST is even
             const uint32_t kt = sm + k_stg * R::kTile, vt = kt + R::kTile;
-            if (a.fault == 2) *abort = 1;
-            if (a.fault == 2 || !warp_wait(smem_u32(&full[k_stg]), phase, abort, a.fault ? 100000 : kWaitCycles)) break;
+            if (!warp_wait(smem_u32(&full[k_stg]), phase, abort, a.fault ? 100000 : kWaitCycles)) break;
             const int64_t j = j0 + i;
             const int64_t left = j < ptiles ? a.inline_prefix - j * kTileKeys : len - (j - ptiles) * kTileKeys;
             const int valid = int(min(left, int64_t(kTileKeys))) - warp * 16;  // of this warp's keys
