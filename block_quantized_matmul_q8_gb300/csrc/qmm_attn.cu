@@ -8,12 +8,14 @@
 // shared out among the CTAs, each streams them through a ring of TMA copies, and each of its 4
 // warps keeps the running softmax of its own 16 keys of every tile, so no warp waits for another.
 // The partial rows stay in shared memory and are joined through the cluster: no second launch
-// and no workspace.  The products run on mma.sync: with 16 rows the copies take an order of
+// and no workspace.  The weights are rounded to the inputs' type for the product with V (its operands
+// have one type; the sum of the weights stays fp32): an error of the size of the output's own
+// rounding.  The products run on mma.sync: with 16 rows the copies take an order of
 // magnitude longer than the tensor work, and tcgen05's 128 rows would stay empty.
 //
 // 48 caches of up to 8192 rows, 32/8 heads of 128: 129 us, 6.35 TB/s (95% of the measured copy
-// rate).  One request of 640 rows: 6 us, of which a tile's copy, products and join take 4 and the
-// launch 2.  64 requests of up to 512 rows after a prefix of 8192: 35 us, the tensor-core phase and
+// rate).  One request of 640 rows: 6.2 us, of which a tile's copy, products and join take 4 and the
+// launch 2.  64 requests of up to 512 rows after a prefix of 8192: 36 us, the tensor-core phase and
 // the caches after one another on most SMs, 4 to 5 us of it starts and joins.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -442,7 +444,10 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // again from L2; read once for all, it costs a second launch and the join of partial rows.  Even
 // where the rereading comes to about 70 MB (32/8 heads of 128, prefix and requests: 1000 x 8, 33 MB,
 // 9.5 us inline and 11.7 on the tensor cores; 1000 x 16, 66 MB, 12.8 and 12.0; 1000 x 32, 131 MB,
-// 18.3 and 12.7; 8192 x 64, 190 and 35).
+// 18.3 and 12.7; 8192 x 64, 190 and 35.  32/32 heads of 64: 1000 x 8, 66 MB, 15.0 and 13.5; 1000 x 16
+// 18.9 and 14.2.  32/2 of 128: 1000 x 40, 41 MB, 16.7 and 17.6; 1000 x 80 23.3 and 18.2).  Heads beyond
+// 16 of a kv head, which read again as blocks of their own, are not counted: 64/2 heads of 128 are
+// even at 20 MB by this count (1000 x 20, 16.6 and 17.6; 1000 x 40 23.3 and 18.2).
 bool prefix_on_tensor_cores(const DecodeArgs &d) {
     return 4.0 * double(d.batch) * double(d.shape.hk) * double(d.prefix) * double(d.shape.d) > 80e6;
 }

@@ -8,6 +8,9 @@
 // the keys in tiles of 128 with the running maximum and sum of a softmax:
 //   S_i = Q_i K_j^T (tcgen05, fp32 in tensor memory)   -> P_i = exp2(scale' (S_i - top)), rounded
 //   to the inputs' type, in tensor memory              -> O_i += P_i V_j (A from tensor memory).
+// The weights are rounded because a 16-bit product takes both operands in one type, V's: that adds
+// an error of the size of the output's own rounding (against 64 bits 1.2 to 1.4 times what one
+// rounding at the end leaves).  The sum of the weights is taken before the rounding, in fp32.
 // While the softmax threads of one half (128 threads, one row each) work, the tensor cores run
 // the other half's two products.  A row's maximum is only moved when a score passes it by more than
 // 2^8 (weights then stay below 256, exact in the fp32 sums), so O_i is rarely rescaled.
@@ -19,10 +22,11 @@
 // Warps: 0-3 and 4-7 softmax of half 0 and 1, 8 copies (TMA), 9 products, 10 gate (it adds the
 // copies' arrival to the weights' barrier), 11 pieces of work.
 //
-// 8192 causal tokens of 32/8 heads of 128, bf16: 335 us, 1640 TFLOP/s, 85% of the measured bf16 rate.
+// 8192 causal tokens of 32/8 heads of 128, bf16: 336 us in a short graph, 1640 TFLOP/s, 85% of the
+// measured bf16 rate; 361 us, 1520 TFLOP/s, 79%, where calls follow one another for long.
 // Of a key tile's 2900 cycles the tensor pipe works on 2048; the rest is the issuing thread (its
 // waits, and products that issue no faster than they run).  24 prompts of 9 to 2048 tokens: 239 us,
-// 1060 TFLOP/s: a piece's last softmax, output and change of piece take about 7000 cycles in which
+// 1060 TFLOP/s (248 in a row of calls): a piece's last softmax, output and change of piece take about 7000 cycles in which
 // the tensor cores run little.  With heads up to 64 a tile takes about 2300 cycles for 1024 of products
 // and as many of exponentials.
 #include <cuda.h>
@@ -196,8 +200,9 @@ __device__ __forceinline__ Tiles tiles_of(const TcArgs &a, int64_t s, int span) 
 }
 
 // The rank'th tile of `span` tokens, most key tiles first (so that the last items to start are
-// short ones), or for many sequences, where that search would take longer than it saves, the
-// last sequence's last tile first.  One warp; false when there is no such tile.
+// short ones; a lane holds a sequence), or for more sequences than lanes the last sequence's last
+// tile first.  One warp; false when there is no such tile.  24 prompts of up to 2048 tokens, 32/8 heads
+// of 128: 222 us sorted, 230 not; 32 of up to 1000: 102.2, 103.3; 8 of up to 500: even.
 constexpr int kSortedSeqs = 32;
 // Where the last search among many sequences ended: a CTA's ranks rise, so that it passes each
 // sequence once (from the last sequence for every piece, 8192 prompts of 4 tokens took 4.8 ms).
@@ -984,7 +989,10 @@ int64_t prompt_tiles(const PromptArgs &p) {
 
 // Key splits of a prompt call: where the tiles would leave half of the SMs or more without work, as
 // many as give each SM an item, of at least four key tiles (counted for sequences of equal lengths:
-// the host does not know theirs).
+// the host does not know theirs; a long chunk beside short prompts is not split).  With parts of at
+// least 2, 4 and 8 tiles, 32/8 heads of 128: 64 tokens on 1300 keys 16.6, 20.0, 22.9 us; on 2100 17.1,
+// 19.2, 24.0; on 4096 19.7, 18.7, 23.5; 128 on 2000 18.5, 21.6, 29.9; 256 on 4000 27.7, 27.6, 30.9: two
+// would be the better bound for most of these.
 int prompt_splits(const PromptArgs &p) {
     const int64_t items = prompt_tiles(p) * p.shape.hk;
     if (items == 0 || p.n_seqs == 0) return 1;
@@ -1037,7 +1045,8 @@ cudaError_t launch_attn_prompt(const PromptArgs &p, qmm_float t, void *ws, cudaS
 }
 
 // The prefix's key splits: enough CTAs (tiles of queries x kv heads x splits) for every SM, at
-// least two key tiles each.
+// least two key tiles each.  With at least 1, 2 and 4, 32/8 heads of 128, requests x prefix: 32 x 700
+// 11.4, 12.6, 17.0 us; 16 x 1300 12.0, 12.8, 16.3; 8 x 2600 13.0, 12.9, 15.3; 4 x 5200 14.0, 14.1, 16.0.
 int attn_prefix_splits(const DecodeArgs &d) {
     const int64_t span = 2 * (kRows / (d.shape.hq / d.shape.hk));
     const int64_t pairs = (d.batch + span - 1) / span * d.shape.hk, tiles = (d.prefix + kKeys - 1) / kKeys;
