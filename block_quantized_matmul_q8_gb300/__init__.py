@@ -37,7 +37,8 @@ EXPORTS = ("qmm_status_string", "qmm_q8_1_bytes", "qmm_row_bytes", "qmm_workspac
            "qmm_get_device_status", "qmm_set_test_fault", "qmm_aligned_row_bytes", "qmm_repack_aligned",
            "qmm_workspace_bytes_aligned", "qmm_mul_mat_aligned", "qmm_workspace_bytes_id_glu", "qmm_mul_mat_id_glu",
            "qmm_qk_norm_rope", "qmm_workspace_bytes_attn_prompt", "qmm_attn_prompt",
-           "qmm_workspace_bytes_attn_decode", "qmm_attn_decode", "qmm_take_attn_error")
+           "qmm_workspace_bytes_attn_decode", "qmm_attn_decode", "qmm_kv_page_bytes", "qmm_kv_append", "qmm_kv_read",
+           "qmm_workspace_bytes_attn_decode_kv", "qmm_attn_decode_kv", "qmm_take_attn_error")
 
 
 class QMMError(RuntimeError):
@@ -59,6 +60,12 @@ class GemmPlan(ctypes.Structure):
 class Heads(ctypes.Structure):
     """A [tokens][heads][head_dim] view (qmm_heads): data pointer and strides in elements."""
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Cache(ctypes.Structure):
+    """A paged key/value cache (qmm_kv_cache)."""
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
 FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 30}
@@ -155,6 +162,18 @@ def lib():
     L.qmm_attn_decode.restype = ctypes.c_int
     L.qmm_attn_decode.argtypes = [HP, HP, HP, I64, I64, P, I64, I64, HP, HP, I64, ctypes.c_int, I64, I64, I64, F32, HP,
                                   P, P, SZ, P]
+    CP = ctypes.POINTER(Cache)
+    L.qmm_kv_page_bytes.restype = SZ
+    L.qmm_kv_page_bytes.argtypes = [ctypes.c_int, I64, I64, I64]
+    L.qmm_kv_append.restype = ctypes.c_int
+    L.qmm_kv_append.argtypes = [HP, HP, HP, ctypes.c_int, I64, I64, I64, I64, P, P, F32, P, P, I64, ctypes.c_int, CP, P,
+                                HP, HP, HP, ctypes.c_int, P]
+    L.qmm_kv_read.restype = ctypes.c_int
+    L.qmm_kv_read.argtypes = [CP, P, I64, I64, P, I64, I64, I64, I64, HP, HP, ctypes.c_int, P]
+    L.qmm_workspace_bytes_attn_decode_kv.restype = SZ
+    L.qmm_workspace_bytes_attn_decode_kv.argtypes = [I64] * 5
+    L.qmm_attn_decode_kv.restype = ctypes.c_int
+    L.qmm_attn_decode_kv.argtypes = [HP, CP, P, I64, I64, P, I64, I64, ctypes.c_int, I64, I64, I64, F32, HP, P, P, SZ, P]
     L.qmm_take_attn_error.restype = ctypes.c_int
     L.qmm_take_attn_error.argtypes = [P, P]
     _lib = L
@@ -675,9 +694,178 @@ def qmm_attn_decode(q: torch.Tensor, k: torch.Tensor | None, v: torch.Tensor | N
     return out
 
 
+def qmm_kv_page_bytes(qtype, page_size: int, heads_kv: int, head_dim: int) -> int:
+    return lib().qmm_kv_page_bytes(_qtype(qtype), page_size, heads_kv, head_dim)
+
+
+class KVPages:
+    """A paged key/value cache in q4_0 or q8_0 over the uint8 CUDA tensor pages [n_pages, page_bytes] (its rows
+    may be apart: the pages of one layer of several), described once for the calls that write and read it."""
+
+    def __init__(self, pages: torch.Tensor, qtype, page_size: int, heads_kv: int, head_dim: int):
+        need = qmm_kv_page_bytes(qtype, page_size, heads_kv, head_dim)
+        if need == 0:
+            raise QMMError(2, "a cache is q4_0 or q8_0, of pages of 16, 32, 64, 128 or 256 tokens and heads of 32, 64, 96 or 128")
+        if not pages.is_cuda:
+            raise QMMError(1, "pages must be a CUDA tensor")
+        if pages.dtype is not torch.uint8:
+            raise QMMError(3, f"pages must be torch.uint8, got {pages.dtype}")
+        if pages.dim() != 2 or pages.shape[1] != need or pages.stride(1) != 1:
+            raise QMMError(2, f"pages must be [n_pages, {need}] with contiguous rows")
+        self.pages, self.qtype, self.page_size, self.heads_kv, self.head_dim = pages, qtype, page_size, heads_kv, head_dim
+        self.device = pages.get_device()
+        self._c = Cache(pages.data_ptr(), pages.shape[0], pages.stride(0), page_size, _qtype(qtype))
+        self._at = ctypes.pointer(self._c)
+
+    @classmethod
+    def empty(cls, n_pages: int, qtype, page_size: int, heads_kv: int, head_dim: int, device="cuda"):
+        """A cache of new pages, whose content is unspecified."""
+        shape = (n_pages, qmm_kv_page_bytes(qtype, page_size, heads_kv, head_dim))
+        return cls(torch.empty(shape, dtype=torch.uint8, device=device), qtype, page_size, heads_kv, head_dim)
+
+
+def _on(device, *tensors):
+    """All tensors on the cache's device, and that device the current one."""
+    if torch._C._cuda_getDevice() != device:
+        raise QMMError(1, f"the cache is on cuda:{device}, which is not the current device")
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise QMMError(1, f"a tensor is on {t.device}, the cache on cuda:{device}")
+
+
+def qmm_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
+                  inv_freq: torch.Tensor | None, cache: KVPages, slots: torch.Tensor, w_q: torch.Tensor | None = None,
+                  w_k: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                  out_dtype=torch.bfloat16, values: bool = False, q_out: torch.Tensor | None = None,
+                  k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+    """qmm_qk_norm_rope with the keys and values written to the cache's slots (int32 [m]: page * page_size +
+    place, -1 for none); returns (q_out, k_out, v_out).  k_out and v_out, what the cache now stands for in
+    out_dtype, are made when `values` is set or either is given, and are None otherwise."""
+    if stream is not None:
+        return _on_stream(stream, functools.partial(qmm_kv_append, q, k, v, positions, inv_freq, cache, slots, w_q, w_k,
+                                                    eps, interleaved, out_dtype, values, q_out, k_out, v_out),
+                          q_out, k_out, v_out)
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
+        raise QMMError(2, "q and k must be [tokens, heads, head_dim]")
+    kv, dtype = k.shape, k.dtype
+    m, hk, d = kv
+    if dtype not in FLOATS or out_dtype not in FLOATS:
+        raise QMMError(3, "k must be fp32, fp16 or bf16")
+    if hk != cache.heads_kv or d != cache.head_dim:
+        raise QMMError(2, f"the cache holds {cache.heads_kv} heads of {cache.head_dim}, k has {hk} of {d}")
+    _on(cache.device, q, k, v, positions, inv_freq, slots, w_q, w_k, q_out, k_out, v_out)
+    hq, shape = 0, None
+    qv = qov = kov = vov = _NO_VIEW
+    if q is not None:
+        hq = q.shape[1]
+        shape = (m, hq, d)
+        if q_out is None:
+            q_out = torch.empty_like(q, dtype=out_dtype, memory_format=torch.contiguous_format)
+        qv, qov = _view(q, "q", shape, dtype), _view(q_out, "q_out", shape, out_dtype)
+    elif q_out is not None:
+        raise QMMError(1, "q_out without q")
+    both = values or k_out is not None or v_out is not None
+    if both:
+        if k_out is None:
+            k_out = torch.empty_like(k, dtype=out_dtype, memory_format=torch.contiguous_format)
+        if v_out is None:
+            v_out = torch.empty_like(v, dtype=out_dtype, memory_format=torch.contiguous_format)
+        kov, vov = _view(k_out, "k_out", kv, out_dtype), _view(v_out, "v_out", kv, out_dtype)
+    _pack6(_views.words, 0, *qv, *_view(k, "k", kv, dtype), *_view(v, "v", kv, dtype), *qov, *kov, *vov)
+    q_, k_, v_, qo, ko, vo = _views.at
+    half = 0 if inv_freq is None else inv_freq.numel()
+    _check(lib().qmm_kv_append(None if q is None else q_, k_, v_, FLOATS[dtype], m, hq, hk, d,
+                               _small(w_q, "w_q", torch.float32, d), _small(w_k, "w_k", torch.float32, d), eps,
+                               _small(positions, "positions", torch.int32, m),
+                               _small(inv_freq, "inv_freq", torch.float32, half), 2 * half, interleaved, cache._at,
+                               _small(slots, "slots", torch.int32, m), None if q is None else qo, ko if both else None,
+                               vo if both else None, FLOATS[out_dtype], _current()), "qmm_kv_append")
+    return q_out, k_out, v_out
+
+
+def _table(table, rows):
+    """(pointer, width, stride) of int32 pages [rows, width]."""
+    if not table.is_cuda or table.dtype is not torch.int32:
+        raise QMMError(1, "the table of pages must be an int32 CUDA tensor")
+    if table.dim() != 2 or table.shape[0] != rows or (table.stride(1) != 1 and table.shape[1] > 1):
+        raise QMMError(2, f"the table of pages must be [{rows}, pages] with contiguous rows")
+    return table.data_ptr(), table.shape[1], table.stride(0)
+
+
+def qmm_kv_read(cache: KVPages, table: torch.Tensor, cu_k: torch.Tensor, tokens: int, out_dtype=torch.bfloat16,
+                k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+    """The sequences of table int32 [n_seqs, pages] as packed rows k and v [tokens, kv_heads, d] in 16 bits, sequence
+    s at rows cu_k[s] to cu_k[s + 1] (int32 [n_seqs + 1]): what qmm_attn_prompt takes."""
+    if stream is not None:
+        return _on_stream(stream, functools.partial(qmm_kv_read, cache, table, cu_k, tokens, out_dtype, k_out, v_out),
+                          k_out, v_out)
+    if out_dtype not in FLOATS:
+        raise QMMError(3, "out_dtype must be fp16 or bf16")
+    _on(cache.device, table, cu_k, k_out, v_out)
+    shape = (tokens, cache.heads_kv, cache.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=out_dtype, device=cache.pages.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=out_dtype, device=cache.pages.device)
+    n = cu_k.numel() - 1
+    _pack4(_views.words, 0, *_view(k_out, "k_out", shape, out_dtype), *_view(v_out, "v_out", shape, out_dtype),
+           *_NO_VIEW, *_NO_VIEW)
+    ko, vo = _views.at[:2]
+    _check(lib().qmm_kv_read(cache._at, *_table(table, n), _small(cu_k, "cu_k", torch.int32, n + 1), n, tokens,
+                             cache.heads_kv, cache.head_dim, ko, vo, FLOATS[out_dtype], _current()), "qmm_kv_read")
+    return k_out, v_out
+
+
+def qmm_workspace_bytes_attn_decode_kv(batch: int, max_len: int, heads_q: int, heads_kv: int, head_dim: int) -> int:
+    return lib().qmm_workspace_bytes_attn_decode_kv(batch, max_len, heads_q, heads_kv, head_dim)
+
+
+def qmm_attn_decode_kv(q: torch.Tensor, cache: KVPages, table: torch.Tensor, lens: torch.Tensor,
+                       max_len: int | None = None, scale: float | None = None, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One query token for each request, q [batch, heads, d] in fp16 or bf16, over the first lens (int32 [batch]) tokens
+    of its pages, table int32 [batch, pages].  max_len bounds lens (None: all that the table holds); a bound
+    close to the lengths is the faster one.  Errors show in qmm_take_attn_error."""
+    if stream is not None:
+        return _on_stream(stream, functools.partial(qmm_attn_decode_kv, q, cache, table, lens, max_len, scale, out, lse,
+                                                    workspace), out)
+    if q.dim() != 3:
+        raise QMMError(2, "q must be [batch, heads, head_dim]")
+    shape, dtype = q.shape, q.dtype
+    b, hq, d = shape
+    if dtype not in FLOATS:
+        raise QMMError(3, "q must be fp16 or bf16")
+    if d != cache.head_dim:
+        raise QMMError(2, f"the cache holds heads of {cache.head_dim}, q has {d}")
+    _on(cache.device, q, table, lens, out, lse, workspace)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    _pack4(_views.words, 0, *_view(q, "q", shape, dtype), *_view(out, "out", shape, dtype), *_NO_VIEW, *_NO_VIEW)
+    q_, o_ = _views.at[:2]
+    table_ptr, width, stride = _table(table, b)
+    if max_len is None:
+        max_len = width * cache.page_size
+    L, hk = lib(), cache.heads_kv
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        ws_bytes = L.qmm_workspace_bytes_attn_decode_kv(b, max_len, hq, hk, d)
+        if ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws_ptr = workspace.data_ptr()
+    _check(L.qmm_attn_decode_kv(q_, cache._at, table_ptr, width, stride, _small(lens, "lens", torch.int32, b), b,
+                                max_len, FLOATS[dtype], hq, hk, d, d ** -0.5 if scale is None else scale, o_,
+                                None if lse is None else _small(lse, "lse", torch.float32, b * hq), ws_ptr, ws_bytes,
+                                _current()), "qmm_attn_decode_kv")
+    return out
+
+
 def qmm_take_attn_error(stream=None) -> int:
-    """8 (QMM_ERR_DEVICE) if any attention call on the current device has given up a wait since the last
-    time this was asked, with or without a workspace of the caller's, else 0 (synchronises the stream)."""
+    """8 (QMM_ERR_DEVICE) if any attention or cache call on the current device has given up a wait since the last
+    time this was asked, with or without a workspace of the caller's, 7 (QMM_ERR_IDS) if one met a page outside
+    its cache, else 0 (synchronises the stream)."""
     v = ctypes.c_int32(0)
     _check(lib().qmm_take_attn_error(ctypes.byref(v), _stream(stream)), "qmm_take_attn_error")
     return v.value

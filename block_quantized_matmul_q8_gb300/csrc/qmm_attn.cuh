@@ -26,18 +26,19 @@ template <typename T> __device__ __forceinline__ uint32_t pack2(float lo, float 
     else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Set by a kernel of this file that gave up a wait, and only taken back by take_gave_up.
-static __device__ int gave_up;
+// Set by a kernel of this file that has an error to report (QMM_ERR_DEVICE: a wait that gave up, QMM_ERR_IDS:
+// a page outside the cache), and only taken back by take_error.
+static __device__ int reported;
 
-// Whether the flag was set on the current device; clears it.  Synchronises the stream.
-static inline cudaError_t take_gave_up(bool *yes, cudaStream_t st) {
+// What the kernels of this file have reported on the current device; clears it.  Synchronises the stream.
+static inline cudaError_t take_error(int *code, cudaStream_t st) {
     int v = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, gave_up, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
+    cudaError_t e = cudaMemcpyFromSymbolAsync(&v, reported, sizeof(v), 0, cudaMemcpyDeviceToHost, st);
     if (e == cudaSuccess) e = cudaStreamSynchronize(st);
-    *yes = v != 0;
+    *code = v;
     if (e != cudaSuccess || !v) return e;
     v = 0;
-    e = cudaMemcpyToSymbolAsync(gave_up, &v, sizeof(v), 0, cudaMemcpyHostToDevice, st);
+    e = cudaMemcpyToSymbolAsync(reported, &v, sizeof(v), 0, cudaMemcpyHostToDevice, st);
     return e == cudaSuccess ? cudaStreamSynchronize(st) : e;
 }
 

@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_tc_kernel(const __grid_con
             if (elect_one()) mma_commit(smem_u32(&bars.drain));
             spin_wait(smem_u32(&bars.drain), 0, &never);
         }
-        if (tid == 0) *a.status = gave_up = QMM_ERR_DEVICE;
+        if (tid == 0) *a.status = reported = QMM_ERR_DEVICE;
         __syncthreads();
     }
     if (warp == 8) tmem_dealloc(tmem, 512);
@@ -1004,7 +1004,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-cudaError_t attn_tc_take_gave_up(bool *yes, cudaStream_t st) { return take_gave_up(yes, st); }
+cudaError_t attn_tc_take_error(int *code, cudaStream_t st) { return take_error(code, st); }
 
 size_t attn_prompt_workspace_bytes(const PromptArgs &p) {
     const size_t splits = prompt_splits(p), rows = size_t(p.tokens_q) * p.shape.hq;

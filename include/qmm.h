@@ -72,7 +72,7 @@ typedef enum {
     QMM_ERR_ALIGN = 4,     /* a pointer not 16-byte aligned */
     QMM_ERR_WORKSPACE = 5, /* workspace smaller than qmm_workspace_bytes() */
     QMM_ERR_CUDA = 6,      /* a CUDA runtime call or kernel launch failed */
-    QMM_ERR_IDS = 7,       /* device status only: a routing id was outside [0, n_experts) */
+    QMM_ERR_IDS = 7,       /* device status only: a routing id was outside [0, n_experts), or a page outside the cache */
     QMM_ERR_DEVICE = 8     /* device status only: a kernel gave up on a bounded wait */
 } qmm_status;
 
@@ -460,9 +460,96 @@ QMM_API qmm_status qmm_attn_decode(const qmm_heads *q, const qmm_heads *k, const
                                    int64_t head_dim, float scale, const qmm_heads *out, float *lse, void *workspace,
                                    size_t ws_bytes, void *stream);
 
-/* Whether any attention call on the current device has given up a bounded wait since the last
- * qmm_take_attn_error: *status is QMM_ERR_DEVICE (the output of a call between the two is
- * unspecified) or QMM_OK.  Calls that succeed do not clear it, reading does, so one read
+/*
+ * A paged cache of keys and values in 4 or 8 bits.  A page holds page_size tokens of heads_kv
+ * heads; which page holds which tokens of which sequence is the caller's table.  Blocks of 32
+ * elements of a head have one scale, as in the weights' formats:
+ *   QMM_Q4_0: d = fp16(e / -8), e the element of largest magnitude (the positive one of two),
+ *             code = x / d to the nearest integer (ties to even) within -8..7;
+ *   QMM_Q8_0: d = fp16(max |x| / 127), code within -127..127;   the cache stands for d * code.
+ * |d| is at most 65504, a d that rounds to 0 holds zeros, NaN is held as 0, infinities as the
+ * largest value of their sign.  Layout of a page: [head][group of 16 tokens][record], a record being
+ *   key codes    [head_dim / E][16 tokens][16 bytes], E = 32 elements (Q4_0: byte i holds elements 2i
+ *                in its low and 2i + 1 in its high nibble, as code + 8) or 16 (Q8_0: code + 128),
+ *   key scales   fp16 [head_dim / 32][16], token j at (j % 8) / 2 * 4 + j % 2 + 2 * (j / 8),
+ *   value codes and value scales alike.
+ * Pages need no initialisation.  One page may stand in several sequences' tables (shared prefixes). */
+typedef struct {
+    void *pages;         /* device, 16-byte aligned */
+    int64_t n_pages;     /* n_pages * page_size < 2^31 */
+    int64_t page_stride; /* bytes from page to page, a multiple of 16, at least qmm_kv_page_bytes */
+    int32_t page_size;   /* tokens of a page: 16, 32, 64, 128 or 256 */
+    int32_t type;        /* QMM_Q4_0 or QMM_Q8_0 */
+} qmm_kv_cache;
+
+/* Bytes of a page; 0 for a type or sizes that the calls reject.  head_dim: a multiple of 32, 32..128. */
+QMM_API size_t qmm_kv_page_bytes(qmm_type t, int64_t page_size, int64_t heads_kv, int64_t head_dim);
+
+/*
+ * qmm_qk_norm_rope into a paged cache: norm and rotation of queries and keys, queries rounded to
+ * out_type, keys and values quantized from fp32 into the cache, one pass.
+ *   slots : int32 [m] on the device: token i goes to page slots[i] / page_size, place slots[i] %
+ *           page_size.  A slot outside [0, n_pages * page_size) (-1 for a padded row) goes to no page.
+ *           Two tokens of a call with the same slot leave that slot's content unspecified.
+ *   q, q_out     : both, or neither (then heads_q is not used).
+ *   k_out, v_out : out_type [m] tokens of heads_kv heads: what the cache now stands for, d * code rounded
+ *           to 16 bits, for attention over the same tokens (qmm_attn_prompt).  Both, or neither.
+ * Everything else as qmm_qk_norm_rope; head_dim a multiple of 32.  q_out may be q itself and k_out
+ * k itself, v_out v itself (same data, strides and type).  Other bytes of the cache stay as they are.
+ */
+QMM_API qmm_status qmm_kv_append(const qmm_heads *q, const qmm_heads *k, const qmm_heads *v, qmm_float in_type,
+                                 int64_t m, int64_t heads_q, int64_t heads_kv, int64_t head_dim, const float *w_q,
+                                 const float *w_k, float eps, const int32_t *positions, const float *inv_freq,
+                                 int64_t rotary_dim, int interleaved, const qmm_kv_cache *cache, const int32_t *slots,
+                                 const qmm_heads *q_out, const qmm_heads *k_out, const qmm_heads *v_out,
+                                 qmm_float out_type, void *stream);
+
+/*
+ * Sequences read back from the cache, packed one after another in 16 bits (the keys and values of
+ * qmm_attn_prompt, for a chunk of a prompt after a history):
+ *   k_out, v_out : out_type [tokens] tokens of heads_kv heads; row cu_k[s] + j is token j of sequence s.
+ *   cu_k  : int32 [n_seqs + 1] on the device, non-decreasing.  Rows outside every sequence are not written.
+ *   table : int32 [n_seqs][table_width] on the device, rows table_stride entries apart: token j of
+ *           sequence s lies in page table[s][j / page_size].
+ * A row whose page is outside [0, n_pages), or beyond the table's width, is zero, and
+ * qmm_take_attn_error says QMM_ERR_IDS.  Each value is rounded once.
+ */
+QMM_API qmm_status qmm_kv_read(const qmm_kv_cache *cache, const int32_t *table, int64_t table_width,
+                               int64_t table_stride, const int32_t *cu_k, int64_t n_seqs, int64_t tokens,
+                               int64_t heads_kv, int64_t head_dim, const qmm_heads *k_out, const qmm_heads *v_out,
+                               qmm_float out_type, void *stream);
+
+/*
+ * Attention of a decoding batch over a paged cache: one query token for each request,
+ *   out[b][h] = softmax over the request's tokens j < lens[b] as in qmm_attn_prompt.
+ *   q, out  : type t [batch] tokens of heads_q heads.
+ *   table   : int32 [batch][table_width] on the device, as in qmm_kv_read; entries past a request's
+ *             last page are not read.
+ *   lens    : int32 [batch] on the device, taken as the nearest value of [0, max_len].
+ *   max_len : at most table_width * page_size: the longest that a request may be (the work is shared
+ *             out for that length, so a bound close to the lengths is the faster one).
+ *   lse     : fp32 [batch][heads_q] or NULL.
+ *   workspace : qmm_workspace_bytes_attn_decode_kv(...) bytes (for the current device), 256-byte aligned; may be
+ *             NULL when that is 0.
+ * A request without tokens gives zeros (lse -infinity).  Cache places past lens[b] have no influence,
+ * whatever they hold.  The tokens of a page outside [0, n_pages) count as not there, and
+ * qmm_take_attn_error says QMM_ERR_IDS.  Heads as for qmm_attn_prompt, head_dim a multiple of 32.
+ * The same inputs on the same GPU give the same bits.  Accuracy, with u = 2^-8 (bf16) or 2^-11 (f16):
+ * |out - exact| <= u |out| + (w + e) sum_j p_j |v_j| + 2^-25 sum_j |code_j| / sum_j exp(s_j - max s), where w
+ * = 2^-10 (bf16: the weight and its product with the value's scale are rounded to fp16) or 2^-11 (f16:
+ * the product alone), the last term is what weights times scales below fp16's normal range lose, and e is that of qmm_attn_prompt.
+ */
+QMM_API size_t qmm_workspace_bytes_attn_decode_kv(int64_t batch, int64_t max_len, int64_t heads_q, int64_t heads_kv,
+                                                  int64_t head_dim);
+QMM_API qmm_status qmm_attn_decode_kv(const qmm_heads *q, const qmm_kv_cache *cache, const int32_t *table,
+                                      int64_t table_width, int64_t table_stride, const int32_t *lens, int64_t batch,
+                                      int64_t max_len, qmm_float t, int64_t heads_q, int64_t heads_kv, int64_t head_dim,
+                                      float scale, const qmm_heads *out, float *lse, void *workspace, size_t ws_bytes,
+                                      void *stream);
+
+/* Whether any attention or cache call on the current device has reported an error since the last
+ * qmm_take_attn_error: *status is QMM_ERR_DEVICE (a bounded wait was given up; the output of a call
+ * between the two is unspecified), QMM_ERR_IDS (a page outside the cache) or QMM_OK.  Calls that succeed do not clear it, reading does, so one read
  * covers all calls of a step, whatever their workspaces.  It synchronises `stream`; a call on
  * another stream is covered once it has run.  Returns QMM_ERR_CUDA if the read fails. */
 QMM_API qmm_status qmm_take_attn_error(int32_t *status, void *stream);
