@@ -44,13 +44,15 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 8;         // query heads of one CTA: the MMA's N side
 constexpr int kMaxCluster = 16;
 constexpr int kMaxFlatBatch = 1024;
-constexpr int kCtas = 4;         // of one SM
+constexpr int kMaxCtas = 5;      // of one SM
 constexpr int kPieceUnits = 4;   // what a piece costs beside its tiles, in tiles
 
 template <bool kQ8, int D> struct Tile {
     static constexpr int kSide = kv_side_bytes(kQ8, D), kScales = kv_scales_at(kQ8, D);
     static constexpr int kRec = kv_record_bytes(kQ8, D), kBytes = 2 * kRec;
-    static constexpr int kStages = std::max(2, std::min(6, 56 * 1024 / (kWarps * kBytes)));
+    // CTAs of an SM: as many as two stages of the ring leave room for, at most five (20 warps of 96 registers)
+    static constexpr int kCtas = std::min(kMaxCtas, 224 * 1024 / (2 * kWarps * kBytes + 4096));
+    static constexpr int kStages = std::min(6, (224 * 1024 / kCtas - 4096) / (kWarps * kBytes));
     static constexpr int kStride = D + 4;  // floats between partial rows
     static constexpr int kRing = kWarps * kStages * kBytes;
     static constexpr int kParts = kWarps * kRows * kStride * 4;  // partial rows, in place of the ring
@@ -63,8 +65,17 @@ struct Args {
     float scale_log2;
     int ctas;               // of the flat form
     float *part, *part_lse; // [ctas][first or last piece][8][d] normalised, their log2 denominators
-    int4 *cuts;             // [ctas]: request, pair, piece and number of parts that begin in the CTA's last piece
+    int4 *cuts;             // what to join: the first part's CTA, its piece, the number of parts, the request's place.  An
+                            // entry for each request and 8 heads, or, where those are more, for each CTA (the last that begins in it)
+    int by_pair;
     int fault;              // as in qmm_attn.cu
+};
+
+// A CTA's next piece of the flat form: some tiles of one request and kv head.
+struct Piece {
+    int64_t b, begin, end, total;  // the request, its first unit, the CTA's last, all units
+    int pair, tiles, first;        // its heads, all its tiles, the first of this CTA
+    int slot, whole;               // 0 for the CTA's first piece, 1 for a later one; whether it is all tiles
 };
 
 __device__ __forceinline__ int request_tiles(const KvDecodeArgs &d, int64_t b) {
@@ -91,10 +102,15 @@ __device__ __forceinline__ float2 halves(uint32_t x) { return __half22float2(*re
 __device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
     return h2bits(__hmul2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y)));
 }
-template <typename T> __device__ __forceinline__ float value(T x);
-template <> __device__ __forceinline__ float value<__half>(__half x) { return __half2float(x); }
-template <> __device__ __forceinline__ float value<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-
+__device__ __forceinline__ uint32_t fma2(uint32_t x, uint32_t y, uint32_t z) {
+    return h2bits(__hfma2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y),
+                          *reinterpret_cast<const __half2 *>(&z)));
+}
+// Two 16-bit values of a word
+template <typename T> __device__ __forceinline__ float2 values(uint32_t x) {
+    if constexpr (std::is_same<T, __half>::value) return halves(x);
+    else return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -102,109 +118,136 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 // c = a b + first
 __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1, const float (&first)[4]) {
+                                          uint32_t b1, float4 first) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(first[0]), "f"(first[1]), "f"(first[2]), "f"(first[3]));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(first.x), "f"(first.y), "f"(first.z), "f"(first.w));
 }
 __device__ __forceinline__ void mma_more(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     const uint32_t a[4] = {a0, a1, a2, a3};
     mma16816<__half>(c, a, b0, b1);
 }
 
-template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_bounds__(kThreads, kCtas) kv_decode_kernel(const __grid_constant__ Args a) {
+template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_bounds__(kThreads, Tile<kQ8, D>::kCtas) kv_decode_kernel(const __grid_constant__ Args a) {
     using L = Tile<kQ8, D>;
     constexpr int ST = L::kStages, NB = D / 32, kQuads = D / 4;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kWarps * ST];
     __shared__ int abort_s;
+    __shared__ Piece piece_s;                        // kept here while the tiles take the registers
     __shared__ float ml_s[kWarps][kRows][2];         // each warp's maximum and sum (log2 domain)
     __shared__ float joined_s[kRows][2];             // the CTA's
     __shared__ float weight_s[kRows][kMaxCluster];
-    __shared__ int warp_sum_s[kWarps];
+    __shared__ uint2 qb_s[NB][2][32];                // B fragments of two MMAs a block: k 2t, 2t + 1 and 2t + 8, 2t + 9 of head g
+    __shared__ uint4 bias_s;                         // -bias as an A operand, of rows g, g + 8, g, g + 8
+    __shared__ float4 qc_s[NB][4];                   // the accumulators' first values, of heads 2t, 2t + 1
     const KvDecodeArgs &d = a.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rank = kFlat ? 0 : (int)cluster_rank(), ranks = kFlat ? 1 : (int)cluster_size();
     const int pairs = d.shape.hk * a.row_blocks;     // of a request
 
     const uint32_t my_ring = smem_u32(ring) + warp * ST * L::kBytes, my_full = smem_u32(full) + warp * ST * 8;
-    if (tid == 0) abort_s = 0;
+    if (kFlat) grid_launch_dependents();  // every CTA stands at once: the join's may take the places that become free
+    if (tid == 0) {
+        abort_s = 0;
+        bias_s = kQ8 ? make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u)
+                     : make_uint4(0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u);
+    }
     if (lane == 0) {
         for (int i = 0; i < ST; ++i) mbar_init(my_full + 8 * i, 2);
         fence_mbar_init();
     }
-    // the pieces: some tiles each of one request and kv head
-    int64_t b, begin = 0, end = 0, total = 1;  // the piece's request, its first unit, the CTA's last, all units
-    int pair, tiles, first = 0;                // its heads, all its tiles, the first of this CTA
+    Piece piece{};
     if (kFlat) {
-        int *const before = reinterpret_cast<int *>(ring);  // units of one head of the requests up to this one
+        // each warp for itself: the sum of all units, then the request that holds the CTA's first
         int sum = 0;
-        for (int base = 0; base < d.batch; base += kThreads) {
-            int v = base + tid < d.batch ? units_of(request_tiles(d, base + tid)) : 0;
+        for (int i = lane; i < d.batch; i += 32) sum += units_of(request_tiles(d, i));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        const int64_t total = int64_t(sum) * pairs, x = cut(total, blockIdx.x, a.ctas);
+        int before = 0, units = kPieceUnits;  // of one head of the requests before the piece's, of that
+        for (int base = 0; base < d.batch; base += 32) {
+            const int own = base + lane < d.batch ? units_of(request_tiles(d, base + lane)) : 0;
+            int upto = own;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, v, s);
-                if (lane >= s) v += u;
+                const int u = __shfl_up_sync(0xffffffffu, upto, s);
+                if (lane >= s) upto += u;
             }
-            if (lane == 31) warp_sum_s[warp] = v;
-            __syncthreads();
-            int here = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) v += sum + here;
-                here += warp_sum_s[w];
+            const uint32_t after = __ballot_sync(0xffffffffu, int64_t(before + upto) * pairs > x);
+            if (after) {
+                const int at = __ffs(after) - 1;
+                piece.b = base + at;
+                units = __shfl_sync(0xffffffffu, own, at);
+                before += __shfl_sync(0xffffffffu, upto, at) - units;
+                break;
             }
-            if (base + tid < d.batch) before[base + tid] = v;
-            sum += here;
-            __syncthreads();
+            before += __shfl_sync(0xffffffffu, upto, 31);
         }
-        total = int64_t(sum) * pairs;
-        const int64_t x = cut(total, blockIdx.x, a.ctas);
-        end = cut(total, blockIdx.x + 1, a.ctas);
-        int lo = 0, hi = (int)d.batch - 1;  // the first request that ends after x
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (int64_t(before[mid]) * pairs > x) hi = mid;
-            else lo = mid + 1;
-        }
-        b = lo;
-        const int start = lo > 0 ? before[lo - 1] : 0, units = max(before[lo] - start, kPieceUnits);
-        tiles = units - kPieceUnits;
-        begin = int64_t(start) * pairs;
-        pair = int((x - begin) / units);
-        begin += int64_t(pair) * units;
-        first = max(int(x - begin) - kPieceUnits, 0);
-        fence_proxy_async_smem();  // the sums' place is the ring from here on
+        piece.total = total;
+        piece.end = cut(total, blockIdx.x + 1, a.ctas);
+        piece.tiles = units - kPieceUnits;
+        piece.begin = int64_t(before) * pairs;
+        piece.pair = int((x - piece.begin) / units);
+        piece.begin += int64_t(piece.pair) * units;
+        piece.first = max(int(x - piece.begin) - kPieceUnits, 0);
+        if (!a.by_pair && tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
     } else {
         const int64_t at = blockIdx.x / ranks;
-        b = at / pairs;
-        pair = int(at - b * pairs);
-        tiles = request_tiles(d, b);
+        piece.b = at / pairs;
+        piece.pair = int(at - piece.b * pairs);
+        piece.tiles = request_tiles(d, piece.b);
     }
-    int4 cut_here = make_int4(0, 0, 0, 0);
     __syncthreads();
     volatile int *abort = &abort_s;
     int stg = 0, phase = 0;  // the warp's next stage
 
-    for (int slot = 0;; slot = 1) {
-        bool whole = true;
+    while (true) {
         int j0, n;  // tiles of the warp
         if (kFlat) {
-            const int count = int(min(end - begin - kPieceUnits, int64_t(tiles))) - first;
+            const int count = int(min(piece.end - piece.begin - kPieceUnits, int64_t(piece.tiles))) - piece.first;
             if (count <= 0) break;
-            whole = count == tiles;
-            if (!whole && first == 0)
-                cut_here = make_int4(int(b), pair, slot, cta_of(total, begin + units_of(tiles) - 1, a.ctas) - int(blockIdx.x) + 1);
-            j0 = first + int(int64_t(count) * warp / kWarps);
-            n = first + int(int64_t(count) * (warp + 1) / kWarps) - j0;
+            piece.whole = count == piece.tiles;
+            if (tid == 0) {
+                piece_s = piece;
+                if (piece.first == 0 && (!piece.whole || a.by_pair)) {
+                    const int64_t place = piece.b * pairs + piece.pair;
+                    const int last = cta_of(piece.total, piece.begin + units_of(piece.tiles) - 1, a.ctas);
+                    a.cuts[a.by_pair ? place : blockIdx.x] =
+                        make_int4(int(blockIdx.x), piece.slot, piece.whole ? 0 : last - int(blockIdx.x) + 1, int(place));
+                }
+            }
+            j0 = piece.first + int(int64_t(count) * warp / kWarps);
+            n = piece.first + int(int64_t(count) * (warp + 1) / kWarps) - j0;
         } else {
+            if (tid == 0) piece_s = piece;
             const int64_t workers = ranks * kWarps, me = rank * kWarps + warp;
-            j0 = int(tiles * me / workers);
-            n = int(tiles * (me + 1) / workers) - j0;
+            j0 = int(piece.tiles * me / workers);
+            n = int(piece.tiles * (me + 1) / workers) - j0;
         }
-        const int hk = pair / a.row_blocks, block = pair - hk * a.row_blocks;
+        const int64_t b = piece.b;
+        const int hk = piece.pair / a.row_blocks, block = piece.pair - hk * a.row_blocks;
         const int head0 = hk * a.group + block * kRows, rows = min(a.group - block * kRows, kRows);
         const int len = (int)min(max(int64_t(d.lens[b]), int64_t(0)), d.max_len);
+
+        // the queries are on their way while the pages are looked up
+        uint2 raw[NB][2];
+        {
+            const T *const src = static_cast<const T *>(d.q) + b * d.sq.t + (head0 + g) * d.sq.h;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                raw[i][0] = raw[i][1] = make_uint2(0, 0);
+                if (g >= rows) continue;
+                if (kQ8) {
+                    raw[i][0] = *reinterpret_cast<const uint2 *>(src + 32 * i + 4 * t);
+                    raw[i][1] = *reinterpret_cast<const uint2 *>(src + 32 * i + 16 + 4 * t);
+                } else {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(src + 32 * i + 8 * t);
+                    raw[i][0] = make_uint2(u.x, u.y);
+                    raw[i][1] = make_uint2(u.z, u.w);
+                }
+            }
+        }
 
         // where the records 2 (j0 + i).. of 16 tiles lie, one a lane, and the pages of the 16 tiles after them: -1 for
         // a page that does not exist, -2 past the last
@@ -222,13 +265,13 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         };
         const uint8_t *src = source(2 * j0 + lane, page_of(2 * j0 + lane));
         int next = page_of(2 * j0 + 32 + lane);
-        uint32_t missing_ahead = __ballot_sync(0xffffffffu, !src), missing = missing_ahead;  // records that are not copied
+        uint32_t missing_ahead = __ballot_sync(0xffffffffu, !src && 2 * j0 + lane < records), missing = 0;  // records that are not copied
         auto issue = [&](int i, int to) {  // the lanes of its two records copy a tile
             if ((i & 15) == 0 && i > 0) {
                 const int record = 2 * (j0 + i) + lane;
                 src = source(record, next);
                 next = page_of(record + 32);
-                missing_ahead = __ballot_sync(0xffffffffu, !src);
+                missing_ahead = __ballot_sync(0xffffffffu, !src && record < records);
             }
             if ((lane >> 1) == (i & 15)) {
                 const uint32_t bar = my_full + 8 * to;
@@ -248,61 +291,70 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, o[D / 16][4];
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        if (n > 0) {
-            uint32_t qb[NB][2][2];  // B fragments of two MMAs a block: k 2t, 2t + 1 and 2t + 8, 2t + 9 of head g
-            float qc[NB][4], factor[2];  // the accumulators' first values
-            {
-                float v[NB][8], most = 0.f;
-                const T *src = static_cast<const T *>(d.q) + b * d.sq.t + (head0 + g) * d.sq.h;
+        float factor[2];  // of heads 2t, 2t + 1
+        {
+            float v[NB][8], most = 0.f;
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
+            for (int i = 0; i < NB; ++i) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        v[i][j] = g < rows ? value<T>(src[32 * i + (kQ8 ? 4 * t + (j & 3) + (j >> 2) * 16 : 8 * t + j)]) : 0.f;
-                        most = fmaxf(most, fabsf(v[i][j]));
-                    }
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                // times 2^up: the largest element into [2^13, 2^14); a negative scale turns the queries
-                const int up = most > 0.f ? max(-100, min(100, 140 - int(__float_as_uint(most) >> 23))) : 0;
-                const float times = copysignf(__int_as_float((127 + up) << 23), a.scale_log2);
-                const float f = fabsf(a.scale_log2) * __int_as_float((127 + 12 - up / 2) << 23) * __int_as_float((127 + 12 - (up - up / 2)) << 23);
-                factor[0] = __shfl_sync(0xffffffffu, f, 8 * t);
-                factor[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    float total = 0.f;
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        // nibbles 0, 4 (and 2, 6) as they are, 1, 5 (and 3, 7) 16 times as large; bytes in order
-                        const float e[4] = {v[i][kQ8 ? 4 * m : 2 * m] * times, v[i][kQ8 ? 4 * m + 1 : 2 * m + 4] * times,
-                                            v[i][kQ8 ? 4 * m + 2 : 2 * m + 1] * (kQ8 ? times : times * 0.0625f),
-                                            v[i][kQ8 ? 4 * m + 3 : 2 * m + 5] * (kQ8 ? times : times * 0.0625f)};
-                        qb[i][m][0] = pack2<__half>(e[0], e[1]);
-                        qb[i][m][1] = pack2<__half>(e[2], e[3]);
-                        const float2 y = halves(qb[i][m][0]), z = halves(qb[i][m][1]);
-                        total += y.x + y.y + (kQ8 ? 1.f : 16.f) * (z.x + z.y);
-                    }
-                    total += __shfl_xor_sync(0xffffffffu, total, 1);
-                    total += __shfl_xor_sync(0xffffffffu, total, 2);
-                    total *= (kQ8 ? -128.f : -8.f) * 0x1p-24f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) qc[i][e] = __shfl_sync(0xffffffffu, total, 8 * t + 4 * (e & 1));
+                for (int j = 0; j < 4; ++j) {
+                    const float2 y = values<T>(j & 1 ? raw[i][j >> 1].y : raw[i][j >> 1].x);
+                    v[i][2 * j] = y.x;
+                    v[i][2 * j + 1] = y.y;
+                    most = fmaxf(most, fmaxf(fabsf(y.x), fabsf(y.y)));
                 }
             }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            // times 2^up: the largest element into [2^13, 2^14); a negative scale turns the queries
+            const int up = most > 0.f ? max(-100, min(100, 140 - int(__float_as_uint(most) >> 23))) : 0;
+            const float times = copysignf(__int_as_float((127 + up) << 23), a.scale_log2);
+            // not zero, so that a score of minus infinity stays one
+            const float f = fmaxf(fabsf(a.scale_log2) * __int_as_float((127 + 12 - up / 2) << 23) * __int_as_float((127 + 12 - (up - up / 2)) << 23), 1e-37f);
+            factor[0] = __shfl_sync(0xffffffffu, f, 8 * t);
+            factor[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                if (i != warp) continue;  // a block a warp
+                float total = 0.f;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    // nibbles 0, 4 (and 2, 6) as they are, 1, 5 (and 3, 7) 16 times as large; bytes in order
+                    const float e[4] = {v[i][kQ8 ? 4 * m : 2 * m] * times, v[i][kQ8 ? 4 * m + 1 : 2 * m + 4] * times,
+                                        v[i][kQ8 ? 4 * m + 2 : 2 * m + 1] * (kQ8 ? times : times * 0.0625f),
+                                        v[i][kQ8 ? 4 * m + 3 : 2 * m + 5] * (kQ8 ? times : times * 0.0625f)};
+                    const uint2 q = make_uint2(pack2<__half>(e[0], e[1]), pack2<__half>(e[2], e[3]));
+                    qb_s[i][m][lane] = q;
+                    const float2 y = halves(q.x), z = halves(q.y);
+                    total += y.x + y.y + (kQ8 ? 1.f : 16.f) * (z.x + z.y);
+                }
+                total += __shfl_xor_sync(0xffffffffu, total, 1);
+                total += __shfl_xor_sync(0xffffffffu, total, 2);
+                total *= (kQ8 ? -128.f : -8.f) * 0x1p-24f;
+                const float c0 = __shfl_sync(0xffffffffu, total, 8 * t), c1 = __shfl_sync(0xffffffffu, total, 8 * t + 4);
+                if (g == 0) qc_s[i][t] = make_float4(c0, c1, c0, c1);
+            }
+        }
+        __syncthreads();
+        if (n > 0) {
             const uint32_t odd = (g & 1) ? 0x7632u : 0x5410u;  // halves of keys g and g + 8 out of four scales
+            uint32_t bias[4];  // read from shared memory once, so that it stays in its registers
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(bias[0]), "=r"(bias[1]), "=r"(bias[2]), "=r"(bias[3])
+                         : "r"(smem_u32(&bias_s)));
+            const int plain = min(n, len / kTileKeys - j0);  // tiles without keys past the end
             bool ok = a.fault != 2;
             int i = 0;
             for (; i < n && ok; ++i) {
                 ok = warp_wait(my_full + 8 * stg, phase, abort, a.fault ? 100000 : kWaitCycles);
                 if (!ok) break;
                 const uint32_t tile = my_ring + stg * L::kBytes;
-                const int valid = len - (j0 + i) * kTileKeys;
-                if ((i & 15) == 0 && i > 0) missing = missing_ahead;
-                const uint32_t lost = (missing >> (2 * (i & 15))) & 3u;
                 uint32_t seen = 0xffffffffu;
-                if (valid < kTileKeys || lost) {
-                    // keys that nobody sees may hold anything: their value scales become zero, their weights too
+                if ((i & 15) == 0) missing = missing_ahead;
+                if (i >= plain || missing) {
+                    // keys that nobody sees may hold anything: their value scales become zero, their scores minus infinity
+                    const int valid = len - (j0 + i) * kTileKeys;
+                    const uint32_t lost = (missing >> (2 * (i & 15))) & 3u;
                     if (valid < kTileKeys) seen = (1u << valid) - 1;
                     if (lost & 1) seen &= 0xffff0000u;
                     if (lost & 2) seen &= 0x0000ffffu;
@@ -317,42 +369,38 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                 }
                 // scores of keys g (first two) and g + 8 of both records, heads 2 t and 2 t + 1
                 float s[2][4];
+                uint32_t f[2][4];  // words of keys 0-7 and 8-15, of two units
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint32_t codes = tile + r * L::kRec;
-                    uint32_t f[4];  // words of keys 0-7 and 8-15, of two units
+                for (int blk = 0; blk < NB; ++blk) {
+                    const uint2 q0 = qb_s[blk][0][lane], q1 = qb_s[blk][1][lane];
+                    const float4 qc = qc_s[blk][t];
 #pragma unroll
-                    for (int blk = 0; blk < NB; ++blk) {
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t codes = tile + r * L::kRec;
                         float acc[4];
-                        const uint32_t(&q0)[2] = qb[blk][0], (&q1)[2] = qb[blk][1];
                         if constexpr (kQ8) {
-                            ldsm4(f, codes + blk * 512 + lane * 16);
-                            mma_first(acc, __byte_perm(f[0], 0, 0x4140), __byte_perm(f[1], 0, 0x4140), __byte_perm(f[0], 0, 0x4342),
-                                      __byte_perm(f[1], 0, 0x4342), q0[0], q0[1], qc[blk]);
-                            mma_more(acc, __byte_perm(f[2], 0, 0x4140), __byte_perm(f[3], 0, 0x4140), __byte_perm(f[2], 0, 0x4342),
-                                     __byte_perm(f[3], 0, 0x4342), q1[0], q1[1]);
+                            ldsm4(f[r], codes + blk * 512 + lane * 16);
+                            const uint32_t(&w)[4] = f[r];
+                            mma_first(acc, __byte_perm(w[0], 0, 0x4140), __byte_perm(w[1], 0, 0x4140), __byte_perm(w[0], 0, 0x4342),
+                                      __byte_perm(w[1], 0, 0x4342), q0.x, q0.y, qc);
+                            mma_more(acc, __byte_perm(w[2], 0, 0x4140), __byte_perm(w[3], 0, 0x4140), __byte_perm(w[2], 0, 0x4342),
+                                     __byte_perm(w[3], 0, 0x4342), q1.x, q1.y);
                         } else {
                             if ((blk & 1) == 0) {
-                                if (blk + 1 < NB) ldsm4(f, codes + blk * 256 + lane * 16);
-                                else ldsm2(f, codes + blk * 256 + (lane & 15) * 16);
+                                if (blk + 1 < NB) ldsm4(f[r], codes + blk * 256 + lane * 16);
+                                else ldsm2(f[r], codes + blk * 256 + (lane & 15) * 16);
                             }
                             constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
-                            const uint32_t y = f[(blk & 1) * 2], z = f[(blk & 1) * 2 + 1];
-                            mma_first(acc, y & lo, z & lo, y & hi, z & hi, q0[0], q0[1], qc[blk]);
-                            mma_more(acc, y >> 8 & lo, z >> 8 & lo, y >> 8 & hi, z >> 8 & hi, q1[0], q1[1]);
+                            const uint32_t y = f[r][(blk & 1) * 2], z = f[r][(blk & 1) * 2 + 1];
+                            mma_first(acc, y & lo, z & lo, y & hi, z & hi, q0.x, q0.y, qc);
+                            mma_more(acc, y >> 8 & lo, z >> 8 & lo, y >> 8 & hi, z >> 8 & hi, q1.x, q1.y);
                         }
                         const uint2 sc = lds64(codes + L::kScales + blk * 32 + (g >> 1) * 8);
                         const float2 ks = halves(__byte_perm(sc.x, sc.y, odd));
-                        if (blk == 0) {
-                            s[r][0] = ks.x * acc[0];
-                            s[r][1] = ks.x * acc[1];
-                            s[r][2] = ks.y * acc[2];
-                            s[r][3] = ks.y * acc[3];
-                        } else {
-                            s[r][0] += ks.x * acc[0];
-                            s[r][1] += ks.x * acc[1];
-                            s[r][2] += ks.y * acc[2];
-                            s[r][3] += ks.y * acc[3];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float y = e < 2 ? ks.x : ks.y;
+                            s[r][e] = blk == 0 ? y * acc[e] : s[r][e] + y * acc[e];
                         }
                     }
                 }
@@ -390,35 +438,31 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
 #pragma unroll
                         for (int e = h; e < 4; e += 2) s[r][e] = ex2(fmaf(s[r][e], factor[h], -base));
                 }
-                if (seen != 0xffffffffu) {  // again, for a factor of zero
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!(seen >> (16 * r + g + 8 * (e >> 1)) & 1u)) s[r][e] = 0.f;
-                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) sum[h] += (s[0][h] + s[0][2 + h]) + (s[1][h] + s[1][2 + h]);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const uint32_t codes = tile + r * L::kRec + L::kSide;
-                    constexpr bool kExact = std::is_same<T, __half>::value;  // one rounding, the output's own is as fine
-                    uint32_t p0 = 0, p1 = 0;
-                    if (!kExact) {
-                        p0 = transpose8x8(pack2<__half>(s[r][0], s[r][1]));
-                        p1 = transpose8x8(pack2<__half>(s[r][2], s[r][3]));
+                    // the weights in the second product's layout: head g, keys 2t, 2t + 1 and 2t + 8, 2t + 9.  For fp16
+                    // outputs what their rounding leaves goes along, so that weight times scale is rounded once
+                    constexpr bool kExact = std::is_same<T, __half>::value;
+                    const uint32_t h0 = pack2<__half>(s[r][0], s[r][1]), h1 = pack2<__half>(s[r][2], s[r][3]);
+                    const uint32_t p0 = transpose8x8(h0), p1 = transpose8x8(h1);
+                    uint32_t l0 = 0, l1 = 0;
+                    if (kExact) {
+                        const float2 y = halves(h0), z = halves(h1);
+                        l0 = transpose8x8(pack2<__half>(s[r][0] - y.x, s[r][1] - y.y));
+                        l1 = transpose8x8(pack2<__half>(s[r][2] - z.x, s[r][3] - z.y));
                     }
                     uint32_t f[4];
 #pragma unroll
                     for (int blk = 0; blk < NB; ++blk) {
-                        uint32_t w0, w1;  // weights times scales of head g, keys 2t, 2t + 1 and 2t + 8, 2t + 9
+                        const uint2 sc = lds64(codes + L::kScales + blk * 32 + t * 8);
+                        uint32_t w0, w1;
                         if (kExact) {
-                            const uint2 sc = lds64(codes + L::kScales + blk * 32 + (g >> 1) * 8);
-                            const float2 vs = halves(__byte_perm(sc.x, sc.y, odd));
-                            w0 = transpose8x8(pack2<__half>(s[r][0] * vs.x, s[r][1] * vs.x));
-                            w1 = transpose8x8(pack2<__half>(s[r][2] * vs.y, s[r][3] * vs.y));
+                            w0 = fma2(p0, sc.x, mul2(l0, sc.x));
+                            w1 = fma2(p1, sc.y, mul2(l1, sc.y));
                         } else {
-                            const uint2 sc = lds64(codes + L::kScales + blk * 32 + t * 8);
                             w0 = mul2(p0, sc.x);
                             w1 = mul2(p1, sc.y);
                         }
@@ -430,7 +474,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                                 const uint32_t y = f[2 * u], z = f[2 * u + 1];
                                 mma_more(o[2 * blk + u], __byte_perm(y, 0, 0x4240), __byte_perm(y, 0, 0x4341), __byte_perm(z, 0, 0x4240),
                                          __byte_perm(z, 0, 0x4341), w0, w1);
-                                mma_more(o[2 * blk + u], 0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u, w0, w1);
+                                mma_more(o[2 * blk + u], bias[0], bias[1], bias[2], bias[3], w0, w1);
                             }
                         } else {
                             if ((blk & 1) == 0) {
@@ -441,8 +485,8 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                             const uint32_t y = f[(blk & 1) * 2], z = f[(blk & 1) * 2 + 1];
                             mma_more(o[2 * blk], y & lo, y & hi, z & lo, z & hi, w0, w1);
                             mma_more(o[2 * blk + 1], y >> 8 & lo, y >> 8 & hi, z >> 8 & lo, z >> 8 & hi, w0, w1);
-                            mma_more(o[2 * blk], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w0, w1);
-                            mma_more(o[2 * blk + 1], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, w0, w1);
+                            mma_more(o[2 * blk], bias[0], bias[1], bias[2], bias[3], w0, w1);
+                            mma_more(o[2 * blk + 1], bias[0], bias[1], bias[2], bias[3], w0, w1);
                         }
                     }
                 }
@@ -476,12 +520,16 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         }
         __syncthreads();  // the ring is free
         const bool gave_up = *abort;
+        piece = piece_s;
+        const int64_t to = piece.b;  // the piece's request and heads again
+        const int to_block = piece.pair % a.row_blocks, to_head = piece.pair / a.row_blocks * a.group + to_block * kRows;
+        const int to_rows = min(a.group - to_block * kRows, kRows);
         float *part = reinterpret_cast<float *>(ring);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int row = 2 * t + h;
             float *dst = part + (warp * kRows + row) * L::kStride;
-            if (row >= rows) continue;
+            if (row >= to_rows) continue;
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
                 constexpr float lo = 0x1p24f, hi = kQ8 ? 0x1p24f : 0x1p20f;  // of rows g, of rows g + 8
@@ -501,8 +549,8 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         if (gave_up && tid == 0) atomicMax(&reported, int(QMM_ERR_DEVICE));
         __syncthreads();
         // the warps' rows joined: the flat form's are done, a cluster's go into the first warp's place
-        const int64_t row0 = b * d.shape.hq + head0;
-        for (int e = tid; e < rows * kQuads; e += kThreads) {
+        const int64_t row0 = to * d.shape.hq + to_head;
+        for (int e = tid; e < to_rows * kQuads; e += kThreads) {
             const int row = e / kQuads, col = (e % kQuads) * 4;
             float m[kWarps], most = -INFINITY;
 #pragma unroll
@@ -525,15 +573,15 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                 const float inv = none ? 0.f : 1.f / total;
                 acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
                 const float log2_total = none ? -INFINITY : base + log2f(total);
-                const int64_t at = (int64_t(blockIdx.x) * 2 + slot) * kRows + row;
-                if (whole) {
-                    T *out = static_cast<T *>(d.out) + b * d.so.t + (head0 + row) * d.so.h + col;
+                const int64_t at = (int64_t(blockIdx.x) * 2 + piece.slot) * kRows + row;
+                if (piece.whole) {
+                    T *out = static_cast<T *>(d.out) + to * d.so.t + (to_head + row) * d.so.h + col;
                     *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
                 } else {
                     *reinterpret_cast<float4 *>(a.part + at * D + col) = acc;
                 }
                 if (col == 0) {
-                    if (!whole) a.part_lse[at] = log2_total;
+                    if (!piece.whole) a.part_lse[at] = log2_total;
                     else if (d.lse) d.lse[row0 + row] = log2_total * kLn2;
                 }
             } else {
@@ -548,13 +596,14 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
             fence_proxy_async_smem();  // the partial rows' place is the ring again
             __syncthreads();
             if (gave_up) break;
-            begin += units_of(tiles);
-            if (begin >= end) break;
-            first = 0;
-            if (++pair == pairs) {
-                pair = 0;
-                do tiles = request_tiles(d, ++b);
-                while (tiles == 0 && b + 1 < d.batch);
+            piece.begin += units_of(piece.tiles);
+            if (piece.begin >= piece.end) break;
+            piece.first = 0;
+            piece.slot = 1;
+            if (++piece.pair == pairs) {
+                piece.pair = 0;
+                do piece.tiles = request_tiles(d, ++piece.b);
+                while (piece.tiles == 0 && piece.b + 1 < d.batch);
             }
             continue;
         }
@@ -562,7 +611,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         else __syncthreads();
 
         // ------------------------------------------------ the cluster's rows
-        for (int row = warp; row < rows; row += kWarps) {
+        for (int row = warp; row < to_rows; row += kWarps) {
             float m = -INFINITY, l = 0.f;
             if (ranks == 1) {
                 m = lane == 0 ? joined_s[row][0] : m;
@@ -584,7 +633,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
             if (lane == 0 && rank == 0 && d.lse) d.lse[row0 + row] = none ? -INFINITY : (base + log2f(total)) * kLn2;
         }
         __syncthreads();
-        for (int e = rank + tid * ranks; e < rows * kQuads; e += ranks * kThreads) {
+        for (int e = rank + tid * ranks; e < to_rows * kQuads; e += ranks * kThreads) {
             const int row = e / kQuads, col = (e % kQuads) * 4;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             const uint32_t addr = smem_u32(part + row * L::kStride + col);
@@ -597,63 +646,94 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                 acc.z += w * y.z;
                 acc.w += w * y.w;
             }
-            T *out = static_cast<T *>(d.out) + b * d.so.t + (head0 + row) * d.so.h + col;
+            T *out = static_cast<T *>(d.out) + to * d.so.t + (to_head + row) * d.so.h + col;
             *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
         }
         if (ranks > 1) cluster_sync();  // no CTA leaves while its shared memory may be read
         break;
     }
-    if (kFlat && tid == 0) a.cuts[blockIdx.x] = cut_here;
 }
 
-// The flat form's requests that were cut, joined: a block for each CTA, which has left word whether such a one
-// begins with it, and a warp a row.  Requests without tiles, which no CTA has seen, give zeros.
-constexpr int kJoinThreads = kRows * 32;
-template <typename T> __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ Args a) {
+// The flat form's requests that were cut, joined: a block for each entry of a.cuts; a row's parts are dealt to
+// blockDim / 256 warps.  Requests without tiles, which no CTA has seen, give zeros.
+constexpr int kJoinGroups = 4;
+template <typename T> __global__ void __launch_bounds__(kRows * kJoinGroups * 32) kv_join_kernel(const __grid_constant__ Args a) {
+    __shared__ float4 acc_s[kJoinGroups][kRows][32];
     const KvDecodeArgs &d = a.d;
-    const int tid = threadIdx.x, row = tid >> 5, lane = tid & 31, D = d.shape.d, col = lane * 4;
+    const int tid = threadIdx.x, row = (tid >> 5) % kRows, group = tid / (32 * kRows), groups = blockDim.x / (32 * kRows);
+    const int lane = tid & 31, D = d.shape.d, col = lane * 4, pairs = d.shape.hk * a.row_blocks;
     for (int64_t b = blockIdx.x; b < d.batch; b += gridDim.x) {
         if (request_tiles(d, b) > 0) continue;
-        for (int e = tid; e < d.shape.hq * (D / 4); e += kJoinThreads) {
+        for (int e = tid; e < d.shape.hq * (D / 4); e += blockDim.x) {
             T *out = static_cast<T *>(d.out) + b * d.so.t + e / (D / 4) * d.so.h + e % (D / 4) * 4;
             *reinterpret_cast<uint2 *>(out) = make_uint2(0, 0);
         }
         if (d.lse)
-            for (int h = tid; h < d.shape.hq; h += kJoinThreads) d.lse[b * d.shape.hq + h] = -INFINITY;
+            for (int h = tid; h < d.shape.hq; h += blockDim.x) d.lse[b * d.shape.hq + h] = -INFINITY;
     }
+    if (a.by_pair && request_tiles(d, blockIdx.x / pairs) == 0) return;  // no CTA has written its entry
     grid_dependency_wait();
     const int4 info = __ldcg(a.cuts + blockIdx.x);
-    const int b = info.x, pair = info.y, parts = info.w;
+    const int parts = info.z, b = info.w / pairs, pair = info.w - b * pairs;
     const int hk = pair / a.row_blocks, block = pair - hk * a.row_blocks;
     const int head = hk * a.group + block * kRows + row;
-    if (parts == 0 || row >= a.group - block * kRows) return;
+    if (parts == 0) return;
+    const int rows = min(a.group - block * kRows, kRows);
     // the first part is the CTA's last piece, the others are the first ones of the CTAs after it
-    auto at = [&](int p) { return (int64_t(blockIdx.x + p) * 2 + (p == 0 ? info.z : 0)) * kRows + row; };
-    float most = -INFINITY, sum = 0.f;
-    for (int p = lane; p < parts; p += 32) most = fmaxf(most, __ldcg(a.part_lse + at(p)));
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
-    const float base = most == -INFINITY ? 0.f : most;
-    for (int p = lane; p < parts; p += 32) sum += ex2(__ldcg(a.part_lse + at(p)) - base);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    auto at = [&](int p) { return (int64_t(info.x + p) * 2 + (p == 0 ? info.y : 0)) * kRows + row; };
+    float most = -INFINITY, sum = 0.f, base = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < parts; p0 += 16) {  // sixteen loads in flight
-        float4 y[16];
-        float w = p0 + lane < parts && lane < 16 ? ex2(__ldcg(a.part_lse + at(p0 + lane)) - base) * inv : 0.f;
+    if (row < rows) {
+        // a group's parts are every fourth one (or all), and the first eight are loaded before their weights are known
+        float l[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            y[i] = col < D && p0 + i < parts ? __ldcg(reinterpret_cast<const float4 *>(a.part + at(p0 + i) * D + col))
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < 8; ++i) l[i] = lane + 32 * i < parts ? __ldcg(a.part_lse + at(lane + 32 * i)) : -INFINITY;
+        float4 y[8];
+        auto load = [&](int p0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float f = __shfl_sync(0xffffffffu, w, i);
-            acc.x += f * y[i].x;
-            acc.y += f * y[i].y;
-            acc.z += f * y[i].z;
-            acc.w += f * y[i].w;
+            for (int i = 0; i < 8; ++i)
+                y[i] = col < D && p0 + i * groups < parts
+                           ? __ldcg(reinterpret_cast<const float4 *>(a.part + at(p0 + i * groups) * D + col))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        load(group);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) most = fmaxf(most, l[i]);
+        for (int p = lane + 256; p < parts; p += 32) most = fmaxf(most, __ldcg(a.part_lse + at(p)));
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
+        base = most == -INFINITY ? 0.f : most;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += ex2(l[i] - base);
+        for (int p = lane + 256; p < parts; p += 32) sum += ex2(__ldcg(a.part_lse + at(p)) - base);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+        for (int p0 = group; p0 < parts; p0 += 8 * groups) {
+            if (p0 != group) load(p0);
+            const int mine = p0 + lane * groups;
+            const float w = lane < 8 && mine < parts ? ex2(__ldcg(a.part_lse + at(mine)) - base) * inv : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = __shfl_sync(0xffffffffu, w, i);
+                acc.x += f * y[i].x;
+                acc.y += f * y[i].y;
+                acc.z += f * y[i].z;
+                acc.w += f * y[i].w;
+            }
         }
+    }
+    if (groups > 1) {
+        acc_s[group][row][lane] = acc;
+        __syncthreads();
+    }
+    if (group != 0 || row >= rows) return;
+    for (int i = 1; i < groups; ++i) {
+        const float4 y = acc_s[i][row][lane];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
     }
     T *out = static_cast<T *>(d.out) + int64_t(b) * d.so.t + head * d.so.h + col;
     if (col < D) *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
@@ -668,12 +748,12 @@ struct Plan {
 };
 Plan plan(const KvDecodeArgs &d) {
     const int64_t group = d.shape.hq / d.shape.hk, pairs = d.batch * d.shape.hk * ((group + kRows - 1) / kRows);
-    const int64_t tiles = (d.max_len + kTileKeys - 1) / kTileKeys, resident = kCtas * device_sm_count();
+    const int64_t tiles = (d.max_len + kTileKeys - 1) / kTileKeys, resident = kMaxCtas * device_sm_count();
     if (d.batch <= kMaxFlatBatch && d.batch * (tiles + kPieceUnits) < (int64_t(1) << 30) && pairs * tiles >= resident * kWarps * 4)
-        return {0, (int)resident};
-    // a power of two, at most a CTA for every four tiles, with room to spare
+        return {0, (int)resident};  // at most: launch() takes as many as the type's and head size's ring lets stand
+    // a power of two, at most a CTA for every four tiles, three an SM
     int ranks = 1;
-    while (ranks < kMaxCluster && tiles >= 2 * ranks * kWarps && pairs * 2 * ranks <= resident - device_sm_count()) ranks *= 2;
+    while (ranks < kMaxCluster && tiles >= 2 * ranks * kWarps && pairs * 2 * ranks <= 3 * device_sm_count()) ranks *= 2;
     return {ranks, 0};
 }
 
@@ -683,10 +763,15 @@ template <typename T, bool kQ8, int D> cudaError_t launch(const Args &a, Plan p,
     cudaError_t e = ensure_smem(kern, L::kSmem);
     if (e != cudaSuccess) return e;
     if (!p.ranks) {
-        kern<<<p.ctas, kThreads, L::kSmem, st>>>(a);
+        Args flat = a;
+        flat.ctas = L::kCtas * device_sm_count();
+        flat.by_pair = pairs <= flat.ctas;
+        kern<<<flat.ctas, kThreads, L::kSmem, st>>>(flat);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        return launch_pdl(kv_join_kernel<T>, dim3((unsigned)p.ctas), dim3(kJoinThreads), 0, st, a);
+        // few entries may have many parts each
+        const int entries = flat.by_pair ? (int)pairs : flat.ctas, groups = entries <= device_sm_count() ? kJoinGroups : 1;
+        return launch_pdl(kv_join_kernel<T>, dim3(entries), dim3(kRows * groups * 32), 0, st, flat);
     }
     if (p.ranks > 8) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
