@@ -43,9 +43,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 8;         // query heads of one CTA: the MMA's N side
 constexpr int kMaxCluster = 16;
-constexpr int kMaxFlatBatch = 1024;
+constexpr int kMaxFlatBatch = 1024, kMaxParts = 1024;
 constexpr int kMaxCtas = 5;      // of one SM
-constexpr int kPieceUnits = 4;   // what a piece costs beside its tiles, in tiles
+constexpr int kPieceUnits = 8;   // what a piece costs beside its tiles, in tiles (128 caches of up to 8192: 129.9 us
+                                 // with 4, 121.7 with 8, 121.6 with 12, 123.8 with 16; 48: 53.6, 50.4, 51.1, 52.1)
 
 template <bool kQ8, int D> struct Tile {
     static constexpr int kSide = kv_side_bytes(kQ8, D), kScales = kv_scales_at(kQ8, D);
@@ -654,15 +655,15 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
     }
 }
 
-// The flat form's requests that were cut, joined: a block for each entry of a.cuts; a row's parts are dealt to
-// blockDim / 256 warps.  Requests without tiles, which no CTA has seen, give zeros.
-constexpr int kJoinGroups = 4;
-template <typename T> __global__ void __launch_bounds__(kRows * kJoinGroups * 32) kv_join_kernel(const __grid_constant__ Args a) {
-    __shared__ float4 acc_s[kJoinGroups][kRows][32];
+// The flat form's requests that were cut, joined: a block for each entry of a.cuts, whose warps share out the
+// rows and then the parts of a row.  Requests without tiles, which no CTA has seen, give zeros.
+constexpr int kJoinWarps = 32;
+template <typename T> __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const __grid_constant__ Args a) {
+    __shared__ float lse_s[kRows * kMaxParts];
+    __shared__ float4 acc_s[kJoinWarps][32];
     const KvDecodeArgs &d = a.d;
-    const int tid = threadIdx.x, row = (tid >> 5) % kRows, group = tid / (32 * kRows), groups = blockDim.x / (32 * kRows);
-    const int lane = tid & 31, D = d.shape.d, col = lane * 4, pairs = d.shape.hk * a.row_blocks;
-    for (int64_t b = blockIdx.x; b < d.batch; b += gridDim.x) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = d.shape.d, col = lane * 4, pairs = d.shape.hk * a.row_blocks;
+    for (int64_t b = blockIdx.x; b < d.batch && blockIdx.y == 0; b += gridDim.x) {
         if (request_tiles(d, b) > 0) continue;
         for (int e = tid; e < d.shape.hq * (D / 4); e += blockDim.x) {
             T *out = static_cast<T *>(d.out) + b * d.so.t + e / (D / 4) * d.so.h + e % (D / 4) * 4;
@@ -675,85 +676,87 @@ template <typename T> __global__ void __launch_bounds__(kRows * kJoinGroups * 32
     grid_dependency_wait();
     const int4 info = __ldcg(a.cuts + blockIdx.x);
     const int parts = info.z, b = info.w / pairs, pair = info.w - b * pairs;
-    const int hk = pair / a.row_blocks, block = pair - hk * a.row_blocks;
-    const int head = hk * a.group + block * kRows + row;
     if (parts == 0) return;
-    const int rows = min(a.group - block * kRows, kRows);
-    // the first part is the CTA's last piece, the others are the first ones of the CTAs after it
-    auto at = [&](int p) { return (int64_t(info.x + p) * 2 + (p == 0 ? info.y : 0)) * kRows + row; };
-    float most = -INFINITY, sum = 0.f, base = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (row < rows) {
-        // a group's parts are every fourth one (or all), and the first eight are loaded before their weights are known
-        float l[8];
+    const int hk = pair / a.row_blocks, block = pair - hk * a.row_blocks;
+    const int head0 = hk * a.group + block * kRows, rows = min(a.group - block * kRows, kRows);
+    // a warp's row, and which of the row's parts: the first part is the CTA's last piece, the others are the
+    // first pieces of the CTAs after it
+    const bool by_row = gridDim.y > 1;  // or a block's one row
+    if (by_row && (int)blockIdx.y >= rows) return;
+    const int groups = by_row ? int(blockDim.x >> 5) : int(blockDim.x >> 5) / rows;
+    const int row = by_row ? blockIdx.y : warp % rows, group = by_row ? warp : warp / rows;
+    auto at = [&](int p) { return (int64_t(info.x + p) * 2 + (p == 0 ? info.y : 0)) * kRows; };
+    float4 y[8], acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto load = [&](int p0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) l[i] = lane + 32 * i < parts ? __ldcg(a.part_lse + at(lane + 32 * i)) : -INFINITY;
-        float4 y[8];
-        auto load = [&](int p0) {
+        for (int i = 0; i < 8; ++i)
+            y[i] = col < D && p0 + i * groups < parts
+                       ? __ldcg(reinterpret_cast<const float4 *>(a.part + (at(p0 + i * groups) + row) * D + col))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    if (group < groups) load(group);
+    for (int e = tid; e < parts * rows; e += blockDim.x) {
+        const int p = e / rows;
+        if (!by_row || e - p * rows == row) lse_s[e] = __ldcg(a.part_lse + at(p) + e - p * rows);
+    }
+    __syncthreads();
+    float most = -INFINITY, sum = 0.f;
+    for (int p = lane; p < parts; p += 32) most = fmaxf(most, lse_s[p * rows + row]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                y[i] = col < D && p0 + i * groups < parts
-                           ? __ldcg(reinterpret_cast<const float4 *>(a.part + at(p0 + i * groups) * D + col))
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-        load(group);
+    for (int s = 16; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
+    const float base = most == -INFINITY ? 0.f : most;
+    for (int p = lane; p < parts; p += 32) sum += ex2(lse_s[p * rows + row] - base);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) most = fmaxf(most, l[i]);
-        for (int p = lane + 256; p < parts; p += 32) most = fmaxf(most, __ldcg(a.part_lse + at(p)));
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, s));
-        base = most == -INFINITY ? 0.f : most;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum += ex2(l[i] - base);
-        for (int p = lane + 256; p < parts; p += 32) sum += ex2(__ldcg(a.part_lse + at(p)) - base);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    if (group < groups)
         for (int p0 = group; p0 < parts; p0 += 8 * groups) {
             if (p0 != group) load(p0);
-            const int mine = p0 + lane * groups;
-            const float w = lane < 8 && mine < parts ? ex2(__ldcg(a.part_lse + at(mine)) - base) * inv : 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float f = __shfl_sync(0xffffffffu, w, i);
-                acc.x += f * y[i].x;
-                acc.y += f * y[i].y;
-                acc.z += f * y[i].z;
-                acc.w += f * y[i].w;
+                const int p = p0 + i * groups;
+                const float w = p < parts ? ex2(lse_s[p * rows + row] - base) * inv : 0.f;
+                acc.x += w * y[i].x;
+                acc.y += w * y[i].y;
+                acc.z += w * y[i].z;
+                acc.w += w * y[i].w;
             }
         }
-    }
     if (groups > 1) {
-        acc_s[group][row][lane] = acc;
+        acc_s[warp][lane] = acc;
         __syncthreads();
     }
-    if (group != 0 || row >= rows) return;
+    if (group != 0) return;
     for (int i = 1; i < groups; ++i) {
-        const float4 y = acc_s[i][row][lane];
-        acc.x += y.x;
-        acc.y += y.y;
-        acc.z += y.z;
-        acc.w += y.w;
+        const float4 z = acc_s[by_row ? i : i * rows + row][lane];
+        acc.x += z.x;
+        acc.y += z.y;
+        acc.z += z.z;
+        acc.w += z.w;
     }
-    T *out = static_cast<T *>(d.out) + int64_t(b) * d.so.t + head * d.so.h + col;
+    T *out = static_cast<T *>(d.out) + int64_t(b) * d.so.t + (head0 + row) * d.so.h + col;
     if (col < D) *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
-    if (d.lse && lane == 0) d.lse[int64_t(b) * d.shape.hq + head] = sum != 0.f ? (base + log2f(sum)) * kLn2 : -INFINITY;
+    if (d.lse && lane == 0) d.lse[int64_t(b) * d.shape.hq + head0 + row] = sum != 0.f ? (base + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// How a call is shared out: clusters of `ranks` CTAs, or the flat form's CTAs (ranks == 0).
+// How a call is shared out: clusters of `ranks` CTAs, or the flat form's CTAs (ranks == 0).  A cluster has a power of
+// two of them, at most one for every four tiles, three an SM in all.  The flat form pays for its cuts (about 4 us and the
+// join's launch) and wins where a warp of a cluster would get 12 tiles of the longest request or more, clusters and flat:
+// 35 requests of up to 1001, 16 heads of 64 in 8 bits (8 tiles) 14.5 and 19.7 us; 256 of 500, 32/8 heads of 128 (4)
+// 30.9 and 36.4; 1 of 12500 (6) 16.1 and 17.3, of 25000 (12) 22.7 and 21.7; 64 of 2000 (16) 26.8 and 27.2; 16 of 8000
+// (31) 40.8 and 25.8; 48 of up to 8192 (32) 83.8 and 50.4.  Its CTAs get 16 tiles at least, so that the join stays small.
 struct Plan {
     int ranks, ctas;
 };
 Plan plan(const KvDecodeArgs &d) {
     const int64_t group = d.shape.hq / d.shape.hk, pairs = d.batch * d.shape.hk * ((group + kRows - 1) / kRows);
-    const int64_t tiles = (d.max_len + kTileKeys - 1) / kTileKeys, resident = kMaxCtas * device_sm_count();
-    if (d.batch <= kMaxFlatBatch && d.batch * (tiles + kPieceUnits) < (int64_t(1) << 30) && pairs * tiles >= resident * kWarps * 4)
-        return {0, (int)resident};  // at most: launch() takes as many as the type's and head size's ring lets stand
-    // a power of two, at most a CTA for every four tiles, three an SM
+    const int64_t tiles = (d.max_len + kTileKeys - 1) / kTileKeys, sms = device_sm_count();
     int ranks = 1;
-    while (ranks < kMaxCluster && tiles >= 2 * ranks * kWarps && pairs * 2 * ranks <= 3 * device_sm_count()) ranks *= 2;
+    while (ranks < kMaxCluster && tiles >= 2 * ranks * kWarps && pairs * 2 * ranks <= 3 * sms) ranks *= 2;
+    if (tiles >= 12 * ranks * kWarps && d.batch <= kMaxFlatBatch && d.batch * (tiles + kPieceUnits) < (int64_t(1) << 30))
+        return {0, (int)std::min({pairs * tiles / 16, kMaxCtas * sms, int64_t(kMaxParts)})};
     return {ranks, 0};
 }
 
@@ -764,14 +767,16 @@ template <typename T, bool kQ8, int D> cudaError_t launch(const Args &a, Plan p,
     if (e != cudaSuccess) return e;
     if (!p.ranks) {
         Args flat = a;
-        flat.ctas = L::kCtas * device_sm_count();
+        flat.ctas = std::min(p.ctas, L::kCtas * device_sm_count());  // what the type and head size let stand at once
         flat.by_pair = pairs <= flat.ctas;
         kern<<<flat.ctas, kThreads, L::kSmem, st>>>(flat);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        // few entries may have many parts each
-        const int entries = flat.by_pair ? (int)pairs : flat.ctas, groups = entries <= device_sm_count() ? kJoinGroups : 1;
-        return launch_pdl(kv_join_kernel<T>, dim3(entries), dim3(kRows * groups * 32), 0, st, flat);
+        // few entries may have many parts each: a block of 32 warps for each row, else one of 8 warps for all
+        const int entries = flat.by_pair ? (int)pairs : flat.ctas;
+        const bool few = entries * kRows <= 2 * device_sm_count();
+        return launch_pdl(kv_join_kernel<T>, dim3(entries, few ? std::min(flat.group, kRows) : 1),
+                          dim3(32 * (few ? kJoinWarps : 8)), 0, st, flat);
     }
     if (p.ranks > 8) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
