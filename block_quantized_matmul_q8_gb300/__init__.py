@@ -724,13 +724,40 @@ class KVPages:
         return cls(torch.empty(shape, dtype=torch.uint8, device=device), qtype, page_size, heads_kv, head_dim)
 
 
-def _on(device, *tensors):
-    """All tensors on the cache's device, and that device the current one."""
-    if torch._C._cuda_getDevice() != device:
-        raise QMMError(1, f"the cache is on cuda:{device}, which is not the current device")
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise QMMError(1, f"a tensor is on {t.device}, the cache on cuda:{device}")
+def _current_device(cache):
+    """The cache's device, which has to be the current one."""
+    if torch._C._cuda_getDevice() != cache.device:
+        raise QMMError(1, f"the cache is on cuda:{cache.device}, which is not the current device")
+    return cache.device
+
+
+def _view_on(device, t: torch.Tensor, name: str, shape, dtype):
+    """_view of a tensor that has to be on `device`."""
+    if t.get_device() != device:
+        raise QMMError(1, f"{name} must be on cuda:{device}, with the cache")
+    if t.dtype is not dtype or t.shape != shape:
+        return _view(t, name, shape, dtype)
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
+        raise QMMError(1, f"{name}: the elements of a head must be contiguous")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _small_on(device, t, name, dtype, numel):
+    """_small of a tensor that has to be on `device`."""
+    if t is None:
+        return None
+    if t.get_device() != device:
+        raise QMMError(1, f"{name} must be on cuda:{device}, with the cache")
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() != numel:
+        return _small(t, name, dtype, numel)
+    return t.data_ptr()
+
+
+def _made(like, dtype, heads, d):
+    """A new contiguous tensor of like's shape [tokens, heads, d], and its view."""
+    out = torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
+    return out, (out.data_ptr(), heads * d, d)
 
 
 def qmm_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor | None,
@@ -753,40 +780,47 @@ def qmm_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, posi
         raise QMMError(3, "k must be fp32, fp16 or bf16")
     if hk != cache.heads_kv or d != cache.head_dim:
         raise QMMError(2, f"the cache holds {cache.heads_kv} heads of {cache.head_dim}, k has {hk} of {d}")
-    _on(cache.device, q, k, v, positions, inv_freq, slots, w_q, w_k, q_out, k_out, v_out)
-    hq, shape = 0, None
-    qv = qov = kov = vov = _NO_VIEW
+    dev = _current_device(cache)
+    kw, vw = _view_on(dev, k, "k", kv, dtype), _view_on(dev, v, "v", kv, dtype)
+    hq = 0
+    qw = qow = kow = vow = _NO_VIEW
     if q is not None:
         hq = q.shape[1]
         shape = (m, hq, d)
+        qw = _view_on(dev, q, "q", shape, dtype)
         if q_out is None:
-            q_out = torch.empty_like(q, dtype=out_dtype, memory_format=torch.contiguous_format)
-        qv, qov = _view(q, "q", shape, dtype), _view(q_out, "q_out", shape, out_dtype)
+            q_out, qow = _made(q, out_dtype, hq, d)
+        else:
+            qow = _view_on(dev, q_out, "q_out", shape, out_dtype)
     elif q_out is not None:
         raise QMMError(1, "q_out without q")
     both = values or k_out is not None or v_out is not None
     if both:
         if k_out is None:
-            k_out = torch.empty_like(k, dtype=out_dtype, memory_format=torch.contiguous_format)
+            k_out, kow = _made(k, out_dtype, hk, d)
+        else:
+            kow = _view_on(dev, k_out, "k_out", kv, out_dtype)
         if v_out is None:
-            v_out = torch.empty_like(v, dtype=out_dtype, memory_format=torch.contiguous_format)
-        kov, vov = _view(k_out, "k_out", kv, out_dtype), _view(v_out, "v_out", kv, out_dtype)
-    _pack6(_views.words, 0, *qv, *_view(k, "k", kv, dtype), *_view(v, "v", kv, dtype), *qov, *kov, *vov)
+            v_out, vow = _made(v, out_dtype, hk, d)
+        else:
+            vow = _view_on(dev, v_out, "v_out", kv, out_dtype)
+    _pack6(_views.words, 0, *qw, *kw, *vw, *qow, *kow, *vow)
     q_, k_, v_, qo, ko, vo = _views.at
     half = 0 if inv_freq is None else inv_freq.numel()
     _check(lib().qmm_kv_append(None if q is None else q_, k_, v_, FLOATS[dtype], m, hq, hk, d,
-                               _small(w_q, "w_q", torch.float32, d), _small(w_k, "w_k", torch.float32, d), eps,
-                               _small(positions, "positions", torch.int32, m),
-                               _small(inv_freq, "inv_freq", torch.float32, half), 2 * half, interleaved, cache._at,
-                               _small(slots, "slots", torch.int32, m), None if q is None else qo, ko if both else None,
-                               vo if both else None, FLOATS[out_dtype], _current()), "qmm_kv_append")
+                               _small_on(dev, w_q, "w_q", torch.float32, d), _small_on(dev, w_k, "w_k", torch.float32, d),
+                               eps, _small_on(dev, positions, "positions", torch.int32, m),
+                               _small_on(dev, inv_freq, "inv_freq", torch.float32, half), 2 * half, interleaved,
+                               cache._at, _small_on(dev, slots, "slots", torch.int32, m), None if q is None else qo,
+                               ko if both else None, vo if both else None, FLOATS[out_dtype], _current()),
+           "qmm_kv_append")
     return q_out, k_out, v_out
 
 
-def _table(table, rows):
+def _table(device, table, rows):
     """(pointer, width, stride) of int32 pages [rows, width]."""
-    if not table.is_cuda or table.dtype is not torch.int32:
-        raise QMMError(1, "the table of pages must be an int32 CUDA tensor")
+    if table.get_device() != device or table.dtype is not torch.int32:
+        raise QMMError(1, "the table of pages must be an int32 CUDA tensor, with the cache")
     if table.dim() != 2 or table.shape[0] != rows or (table.stride(1) != 1 and table.shape[1] > 1):
         raise QMMError(2, f"the table of pages must be [{rows}, pages] with contiguous rows")
     return table.data_ptr(), table.shape[1], table.stride(0)
@@ -801,23 +835,33 @@ def qmm_kv_read(cache: KVPages, table: torch.Tensor, cu_k: torch.Tensor, tokens:
                           k_out, v_out)
     if out_dtype not in FLOATS:
         raise QMMError(3, "out_dtype must be fp16 or bf16")
-    _on(cache.device, table, cu_k, k_out, v_out)
-    shape = (tokens, cache.heads_kv, cache.head_dim)
+    dev, hk, d = _current_device(cache), cache.heads_kv, cache.head_dim
+    shape = (tokens, hk, d)
     if k_out is None:
         k_out = torch.empty(shape, dtype=out_dtype, device=cache.pages.device)
+        kow = (k_out.data_ptr(), hk * d, d)
+    else:
+        kow = _view_on(dev, k_out, "k_out", shape, out_dtype)
     if v_out is None:
         v_out = torch.empty(shape, dtype=out_dtype, device=cache.pages.device)
+        vow = (v_out.data_ptr(), hk * d, d)
+    else:
+        vow = _view_on(dev, v_out, "v_out", shape, out_dtype)
     n = cu_k.numel() - 1
-    _pack4(_views.words, 0, *_view(k_out, "k_out", shape, out_dtype), *_view(v_out, "v_out", shape, out_dtype),
-           *_NO_VIEW, *_NO_VIEW)
-    ko, vo = _views.at[:2]
-    _check(lib().qmm_kv_read(cache._at, *_table(table, n), _small(cu_k, "cu_k", torch.int32, n + 1), n, tokens,
-                             cache.heads_kv, cache.head_dim, ko, vo, FLOATS[out_dtype], _current()), "qmm_kv_read")
+    _pack4(_views.words, 0, *kow, *vow, *_NO_VIEW, *_NO_VIEW)
+    at = _views.at
+    _check(lib().qmm_kv_read(cache._at, *_table(dev, table, n), _small_on(dev, cu_k, "cu_k", torch.int32, n + 1), n, tokens,
+                             hk, d, at[0], at[1], FLOATS[out_dtype], _current()), "qmm_kv_read")
     return k_out, v_out
 
 
 def qmm_workspace_bytes_attn_decode_kv(batch: int, max_len: int, heads_q: int, heads_kv: int, head_dim: int) -> int:
     return lib().qmm_workspace_bytes_attn_decode_kv(batch, max_len, heads_q, heads_kv, head_dim)
+
+
+@functools.lru_cache(maxsize=4096)
+def _decode_kv_bytes(device, *sizes):
+    return lib().qmm_workspace_bytes_attn_decode_kv(*sizes)
 
 
 def qmm_attn_decode_kv(q: torch.Tensor, cache: KVPages, table: torch.Tensor, lens: torch.Tensor,
@@ -837,28 +881,32 @@ def qmm_attn_decode_kv(q: torch.Tensor, cache: KVPages, table: torch.Tensor, len
         raise QMMError(3, "q must be fp16 or bf16")
     if d != cache.head_dim:
         raise QMMError(2, f"the cache holds heads of {cache.head_dim}, q has {d}")
-    _on(cache.device, q, table, lens, out, lse, workspace)
+    dev, hk = _current_device(cache), cache.heads_kv
+    qw = _view_on(dev, q, "q", shape, dtype)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    _pack4(_views.words, 0, *_view(q, "q", shape, dtype), *_view(out, "out", shape, dtype), *_NO_VIEW, *_NO_VIEW)
-    q_, o_ = _views.at[:2]
-    table_ptr, width, stride = _table(table, b)
+        out, ow = _made(q, dtype, hq, d)
+    else:
+        ow = _view_on(dev, out, "out", shape, dtype)
+    _pack4(_views.words, 0, *qw, *ow, *_NO_VIEW, *_NO_VIEW)
+    at = _views.at
+    table_ptr, width, stride = _table(dev, table, b)
     if max_len is None:
         max_len = width * cache.page_size
-    L, hk = lib(), cache.heads_kv
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         _dev(workspace, "workspace")
+        if workspace.get_device() != dev:
+            raise QMMError(1, f"workspace must be on cuda:{dev}, with the cache")
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
-        ws_bytes = L.qmm_workspace_bytes_attn_decode_kv(b, max_len, hq, hk, d)
+        ws_bytes = _decode_kv_bytes(dev, b, max_len, hq, hk, d)
         if ws_bytes:
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
             ws_ptr = workspace.data_ptr()
-    _check(L.qmm_attn_decode_kv(q_, cache._at, table_ptr, width, stride, _small(lens, "lens", torch.int32, b), b,
-                                max_len, FLOATS[dtype], hq, hk, d, d ** -0.5 if scale is None else scale, o_,
-                                None if lse is None else _small(lse, "lse", torch.float32, b * hq), ws_ptr, ws_bytes,
-                                _current()), "qmm_attn_decode_kv")
+    _check(lib().qmm_attn_decode_kv(at[0], cache._at, table_ptr, width, stride, _small_on(dev, lens, "lens", torch.int32, b),
+                                    b, max_len, FLOATS[dtype], hq, hk, d, d ** -0.5 if scale is None else scale, at[1],
+                                    _small_on(dev, lse, "lse", torch.float32, b * hq), ws_ptr, ws_bytes, _current()),
+           "qmm_attn_decode_kv")
     return out
 
 
