@@ -44,14 +44,15 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 8;         // query heads of one CTA: the MMA's N side
 constexpr int kMaxCluster = 16;
 constexpr int kMaxFlatBatch = 1024, kMaxParts = 1024;
-constexpr int kMaxCtas = 5;      // of one SM
-constexpr int kPieceUnits = 8;   // what a piece costs beside its tiles, in tiles (128 caches of up to 8192: 129.9 us
-                                 // with 4, 121.7 with 8, 121.6 with 12, 123.8 with 16; 48: 53.6, 50.4, 51.1, 52.1)
+constexpr int kMaxCtas = 4;      // of one SM
+constexpr int kPieceUnits = 12;  // what a piece costs beside its tiles, in tiles (128 caches of up to 8192: 114.9 us
+                                 // with 8, 111.8 with 12; 256 of up to 2000: 71.9 and 69.1; 48 of 8192 even)
 
 template <bool kQ8, int D> struct Tile {
     static constexpr int kSide = kv_side_bytes(kQ8, D), kScales = kv_scales_at(kQ8, D);
     static constexpr int kRec = kv_record_bytes(kQ8, D), kBytes = 2 * kRec;
-    // CTAs of an SM: as many as two stages of the ring leave room for, at most five (20 warps of 96 registers)
+    // CTAs of an SM: as many as two stages of the ring leave room for, at most four: 16 warps of 128 registers (with
+    // five CTAs of 96 registers 128 caches took 122.4 us instead of 115.2, with three 119.3)
     static constexpr int kCtas = std::min(kMaxCtas, 224 * 1024 / (2 * kWarps * kBytes + 4096));
     static constexpr int kStages = std::min(6, (224 * 1024 / kCtas - 4096) / (kWarps * kBytes));
     static constexpr int kStride = D + 4;  // floats between partial rows
@@ -140,7 +141,6 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
     __shared__ float joined_s[kRows][2];             // the CTA's
     __shared__ float weight_s[kRows][kMaxCluster];
     __shared__ uint2 qb_s[NB][2][32];                // B fragments of two MMAs a block: k 2t, 2t + 1 and 2t + 8, 2t + 9 of head g
-    __shared__ uint4 bias_s;                         // -bias as an A operand, of rows g, g + 8, g, g + 8
     __shared__ float4 qc_s[NB][4];                   // the accumulators' first values, of heads 2t, 2t + 1
     const KvDecodeArgs &d = a.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -149,11 +149,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
 
     const uint32_t my_ring = smem_u32(ring) + warp * ST * L::kBytes, my_full = smem_u32(full) + warp * ST * 8;
     if (kFlat) grid_launch_dependents();  // every CTA stands at once: the join's may take the places that become free
-    if (tid == 0) {
-        abort_s = 0;
-        bias_s = kQ8 ? make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u)
-                     : make_uint4(0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u);
-    }
+    if (tid == 0) abort_s = 0;
     if (lane == 0) {
         for (int i = 0; i < ST; ++i) mbar_init(my_full + 8 * i, 2);
         fence_mbar_init();
@@ -339,10 +335,8 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         __syncthreads();
         if (n > 0) {
             const uint32_t odd = (g & 1) ? 0x7632u : 0x5410u;  // halves of keys g and g + 8 out of four scales
-            uint32_t bias[4];  // read from shared memory once, so that it stays in its registers
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(bias[0]), "=r"(bias[1]), "=r"(bias[2]), "=r"(bias[3])
-                         : "r"(smem_u32(&bias_s)));
+            // -bias as an A operand, of rows g, g + 8, g, g + 8
+            constexpr uint32_t kBias[4] = {kQ8 ? 0x80808080u : 0x80088008u, 0x80808080u, kQ8 ? 0x80808080u : 0x80088008u, 0x80808080u};
             const int plain = min(n, len / kTileKeys - j0);  // tiles without keys past the end
             bool ok = a.fault != 2;
             int i = 0;
@@ -475,7 +469,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                                 const uint32_t y = f[2 * u], z = f[2 * u + 1];
                                 mma_more(o[2 * blk + u], __byte_perm(y, 0, 0x4240), __byte_perm(y, 0, 0x4341), __byte_perm(z, 0, 0x4240),
                                          __byte_perm(z, 0, 0x4341), w0, w1);
-                                mma_more(o[2 * blk + u], bias[0], bias[1], bias[2], bias[3], w0, w1);
+                                mma_more(o[2 * blk + u], kBias[0], kBias[1], kBias[2], kBias[3], w0, w1);
                             }
                         } else {
                             if ((blk & 1) == 0) {
@@ -486,8 +480,8 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                             const uint32_t y = f[(blk & 1) * 2], z = f[(blk & 1) * 2 + 1];
                             mma_more(o[2 * blk], y & lo, y & hi, z & lo, z & hi, w0, w1);
                             mma_more(o[2 * blk + 1], y >> 8 & lo, y >> 8 & hi, z >> 8 & lo, z >> 8 & hi, w0, w1);
-                            mma_more(o[2 * blk], bias[0], bias[1], bias[2], bias[3], w0, w1);
-                            mma_more(o[2 * blk + 1], bias[0], bias[1], bias[2], bias[3], w0, w1);
+                            mma_more(o[2 * blk], kBias[0], kBias[1], kBias[2], kBias[3], w0, w1);
+                            mma_more(o[2 * blk + 1], kBias[0], kBias[1], kBias[2], kBias[3], w0, w1);
                         }
                     }
                 }
