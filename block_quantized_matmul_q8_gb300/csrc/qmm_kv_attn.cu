@@ -14,7 +14,7 @@
 //   - keys are the MMA's 16 rows and query heads its 8 columns, so that no row is empty; the weights reach the
 //     second product's layout by movmatrix.  Codes come by ldmatrix with neighbouring codes in one 16-bit unit,
 //     transposed for V, so that a nibble's mask gives the pairs of keys or elements that the MMA wants.
-// A warp takes tiles of 32 keys on its own: a private ring of bulk copies (a record of 16 tokens is
+// A warp takes tiles of 32 keys (64 of small heads) on its own: a private ring of bulk copies (a record of 16 tokens is
 // contiguous), its running softmax, no barrier with other warps until the join.
 //
 // Two ways to share the work out.  Calls that fit the SMs at once: a cluster of up to 16 CTAs takes one request
@@ -38,7 +38,6 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTileKeys = 32;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 8;         // query heads of one CTA: the MMA's N side
@@ -50,7 +49,10 @@ constexpr int kPieceUnits = 12;  // what a piece costs beside its tiles, in tile
 
 template <bool kQ8, int D> struct Tile {
     static constexpr int kSide = kv_side_bytes(kQ8, D), kScales = kv_scales_at(kQ8, D);
-    static constexpr int kRec = kv_record_bytes(kQ8, D), kBytes = 2 * kRec;
+    static constexpr int kRec = kv_record_bytes(kQ8, D);
+    // Records of a tile: what a tile costs beside its records is spread over 2.3 KB or more
+    static constexpr int kRecs = 2 * kRec < 2400 ? 4 : 2, kKeys = kRecs * kKvGroup, kBytes = kRecs * kRec;
+    static constexpr int kWindow = 32 / kRecs;  // tiles whose records' places the 32 lanes hold
     // CTAs of an SM: as many as two stages of the ring leave room for, at most four: 16 warps of 128 registers (with
     // five CTAs of 96 registers 128 caches took 122.4 us instead of 115.2, with three 119.3)
     static constexpr int kCtas = std::min(kMaxCtas, 224 * 1024 / (2 * kWarps * kBytes + 4096));
@@ -80,8 +82,8 @@ struct Piece {
     int slot, whole;               // 0 for the CTA's first piece, 1 for a later one; whether it is all tiles
 };
 
-__device__ __forceinline__ int request_tiles(const KvDecodeArgs &d, int64_t b) {
-    return (int)((min(max(int64_t(d.lens[b]), int64_t(0)), d.max_len) + kTileKeys - 1) / kTileKeys);
+__device__ __forceinline__ int request_len(const KvDecodeArgs &d, int64_t b) {
+    return (int)min(max(int64_t(d.lens[b]), int64_t(0)), d.max_len);
 }
 // The flat form's row has kPieceUnits units and one for each tile for every request and kv head, so that
 // a CTA of many short pieces gets fewer tiles.  CTA c takes the units [total c / ctas, total (c + 1) / ctas) of it.
@@ -132,7 +134,7 @@ __device__ __forceinline__ void mma_more(float (&c)[4], uint32_t a0, uint32_t a1
 
 template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_bounds__(kThreads, Tile<kQ8, D>::kCtas) kv_decode_kernel(const __grid_constant__ Args a) {
     using L = Tile<kQ8, D>;
-    constexpr int ST = L::kStages, NB = D / 32, kQuads = D / 4;
+    constexpr int ST = L::kStages, NB = D / 32, kQuads = D / 4, R = L::kRecs;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kWarps * ST];
     __shared__ int abort_s;
@@ -143,6 +145,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
     __shared__ uint2 qb_s[NB][2][32];                // B fragments of two MMAs a block: k 2t, 2t + 1 and 2t + 8, 2t + 9 of head g
     __shared__ float4 qc_s[NB][4];                   // the accumulators' first values, of heads 2t, 2t + 1
     const KvDecodeArgs &d = a.d;
+    auto request_tiles = [&](int64_t b) { return (request_len(d, b) + L::kKeys - 1) / L::kKeys; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rank = kFlat ? 0 : (int)cluster_rank(), ranks = kFlat ? 1 : (int)cluster_size();
     const int pairs = d.shape.hk * a.row_blocks;     // of a request
@@ -151,20 +154,20 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
     if (kFlat) grid_launch_dependents();  // every CTA stands at once: the join's may take the places that become free
     if (tid == 0) abort_s = 0;
     if (lane == 0) {
-        for (int i = 0; i < ST; ++i) mbar_init(my_full + 8 * i, 2);
+        for (int i = 0; i < ST; ++i) mbar_init(my_full + 8 * i, R);
         fence_mbar_init();
     }
     Piece piece{};
     if (kFlat) {
         // each warp for itself: the sum of all units, then the request that holds the CTA's first
         int sum = 0;
-        for (int i = lane; i < d.batch; i += 32) sum += units_of(request_tiles(d, i));
+        for (int i = lane; i < d.batch; i += 32) sum += units_of(request_tiles(i));
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
         const int64_t total = int64_t(sum) * pairs, x = cut(total, blockIdx.x, a.ctas);
         int before = 0, units = kPieceUnits;  // of one head of the requests before the piece's, of that
         for (int base = 0; base < d.batch; base += 32) {
-            const int own = base + lane < d.batch ? units_of(request_tiles(d, base + lane)) : 0;
+            const int own = base + lane < d.batch ? units_of(request_tiles(base + lane)) : 0;
             int upto = own;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
@@ -193,7 +196,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         const int64_t at = blockIdx.x / ranks;
         piece.b = at / pairs;
         piece.pair = int(at - piece.b * pairs);
-        piece.tiles = request_tiles(d, piece.b);
+        piece.tiles = request_tiles(piece.b);
     }
     __syncthreads();
     volatile int *abort = &abort_s;
@@ -225,7 +228,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         const int64_t b = piece.b;
         const int hk = piece.pair / a.row_blocks, block = piece.pair - hk * a.row_blocks;
         const int head0 = hk * a.group + block * kRows, rows = min(a.group - block * kRows, kRows);
-        const int len = (int)min(max(int64_t(d.lens[b]), int64_t(0)), d.max_len);
+        const int len = request_len(d, b);
 
         // the queries are on their way while the pages are looked up
         uint2 raw[NB][2];
@@ -246,9 +249,9 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
             }
         }
 
-        // where the records 2 (j0 + i).. of 16 tiles lie, one a lane, and the pages of the 16 tiles after them: -1 for
+        // where the records R (j0 + i).. of the next 32 lie, one a lane, and the pages of the 32 after them: -1 for
         // a page that does not exist, -2 past the last
-        const int log2g = d.cache.page_log2 - 4, records = min((len + 15) / 16, 2 * (j0 + n));
+        const int log2g = d.cache.page_log2 - 4, records = min((len + 15) / 16, R * (j0 + n));
         const int32_t *const table = d.table + b * d.table_stride;
         auto page_of = [&](int record) {
             if (record >= records) return -2;
@@ -260,21 +263,21 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
             const int64_t at = (int64_t(hk) << log2g) + (record & ((1 << log2g) - 1));
             return page >= 0 ? d.cache.pages + page * d.cache.page_stride + at * L::kRec : nullptr;
         };
-        const uint8_t *src = source(2 * j0 + lane, page_of(2 * j0 + lane));
-        int next = page_of(2 * j0 + 32 + lane);
-        uint32_t missing_ahead = __ballot_sync(0xffffffffu, !src && 2 * j0 + lane < records), missing = 0;  // records that are not copied
-        auto issue = [&](int i, int to) {  // the lanes of its two records copy a tile
-            if ((i & 15) == 0 && i > 0) {
-                const int record = 2 * (j0 + i) + lane;
+        const uint8_t *src = source(R * j0 + lane, page_of(R * j0 + lane));
+        int next = page_of(R * j0 + 32 + lane);
+        uint32_t missing_ahead = __ballot_sync(0xffffffffu, !src && R * j0 + lane < records), missing = 0;  // records that are not copied
+        auto issue = [&](int i, int to) {  // the lanes of its records copy a tile
+            if ((i & (L::kWindow - 1)) == 0 && i > 0) {
+                const int record = R * (j0 + i) + lane;
                 src = source(record, next);
                 next = page_of(record + 32);
                 missing_ahead = __ballot_sync(0xffffffffu, !src && record < records);
             }
-            if ((lane >> 1) == (i & 15)) {
+            if (lane / R == (i & (L::kWindow - 1))) {
                 const uint32_t bar = my_full + 8 * to;
                 if (src) {
                     mbar_arrive_expect_tx(bar, L::kRec);
-                    bulk_g2s(my_ring + to * L::kBytes + (lane & 1) * L::kRec, src, L::kRec, bar);
+                    bulk_g2s(my_ring + to * L::kBytes + (lane & (R - 1)) * L::kRec, src, L::kRec, bar);
                 } else {
                     mbar_arrive(bar);
                 }
@@ -337,23 +340,24 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
             const uint32_t odd = (g & 1) ? 0x7632u : 0x5410u;  // halves of keys g and g + 8 out of four scales
             // -bias as an A operand, of rows g, g + 8, g, g + 8
             constexpr uint32_t kBias[4] = {kQ8 ? 0x80808080u : 0x80088008u, 0x80808080u, kQ8 ? 0x80808080u : 0x80088008u, 0x80808080u};
-            const int plain = min(n, len / kTileKeys - j0);  // tiles without keys past the end
+            const int plain = min(n, len / L::kKeys - j0);  // tiles without keys past the end
             bool ok = a.fault != 2;
             int i = 0;
             for (; i < n && ok; ++i) {
                 ok = warp_wait(my_full + 8 * stg, phase, abort, a.fault ? 100000 : kWaitCycles);
                 if (!ok) break;
                 const uint32_t tile = my_ring + stg * L::kBytes;
-                uint32_t seen = 0xffffffffu;
-                if ((i & 15) == 0) missing = missing_ahead;
-                if (i >= plain || missing) {
+                if ((i & (L::kWindow - 1)) == 0) missing = missing_ahead;
+                const bool care = i >= plain || missing;
+                uint64_t seen = ~uint64_t(0);
+                if (care) {
                     // keys that nobody sees may hold anything: their value scales become zero, their scores minus infinity
-                    const int valid = len - (j0 + i) * kTileKeys;
-                    const uint32_t lost = (missing >> (2 * (i & 15))) & 3u;
-                    if (valid < kTileKeys) seen = (1u << valid) - 1;
-                    if (lost & 1) seen &= 0xffff0000u;
-                    if (lost & 2) seen &= 0x0000ffffu;
-                    for (int e = lane; e < 2 * NB * 16; e += 32) {
+                    const int valid = len - (j0 + i) * L::kKeys;
+                    if (valid < L::kKeys) seen = (uint64_t(1) << valid) - 1;
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (missing >> (R * (i & (L::kWindow - 1)) + r) & 1u) seen &= ~(uint64_t(0xffff) << (16 * r));
+                    for (int e = lane; e < R * NB * 16; e += 32) {
                         const int rec = e / (NB * 16), at = e % (NB * 16), place = at & 15;
                         const int token = 2 * (place >> 2) + (place & 1) + 8 * ((place >> 1) & 1);
                         if (!(seen >> (16 * rec + token) & 1u))
@@ -362,15 +366,15 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                // scores of keys g (first two) and g + 8 of both records, heads 2 t and 2 t + 1
-                float s[2][4];
-                uint32_t f[2][4];  // words of keys 0-7 and 8-15, of two units
+                // scores of keys g (first two) and g + 8 of the records, heads 2 t and 2 t + 1
+                float s[R][4];
+                uint32_t f[R][4];  // words of keys 0-7 and 8-15, of two units
 #pragma unroll
                 for (int blk = 0; blk < NB; ++blk) {
                     const uint2 q0 = qb_s[blk][0][lane], q1 = qb_s[blk][1][lane];
                     const float4 qc = qc_s[blk][t];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
+                    for (int r = 0; r < R; ++r) {
                         const uint32_t codes = tile + r * L::kRec;
                         float acc[4];
                         if constexpr (kQ8) {
@@ -399,16 +403,20 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                         }
                     }
                 }
-                if (seen != 0xffffffffu) {
+                if (care) {
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
+                    for (int r = 0; r < R; ++r)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (!(seen >> (16 * r + g + 8 * (e >> 1)) & 1u)) s[r][e] = -INFINITY;
                 }
                 float m[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) m[h] = fmaxf(fmaxf(s[0][h], s[0][2 + h]), fmaxf(s[1][h], s[1][2 + h]));
+                for (int h = 0; h < 2; ++h) {
+                    m[h] = fmaxf(s[0][h], s[0][2 + h]);
+#pragma unroll
+                    for (int r = 1; r < R; ++r) m[h] = fmaxf(m[h], fmaxf(s[r][h], s[r][2 + h]));
+                }
                 if (__any_sync(0xffffffffu, m[0] > top[0] || m[1] > top[1])) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -429,14 +437,16 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                 for (int h = 0; h < 2; ++h) {
                     const float base = top[h] == -INFINITY ? 0.f : top[h] * factor[h];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
+                    for (int r = 0; r < R; ++r)
 #pragma unroll
                         for (int e = h; e < 4; e += 2) s[r][e] = ex2(fmaf(s[r][e], factor[h], -base));
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) sum[h] += (s[0][h] + s[0][2 + h]) + (s[1][h] + s[1][2 + h]);
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
+                    for (int h = 0; h < 2; ++h) sum[h] += s[r][h] + s[r][2 + h];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
                     const uint32_t codes = tile + r * L::kRec + L::kSide;
                     // the weights in the second product's layout: head g, keys 2t, 2t + 1 and 2t + 8, 2t + 9.  For fp16
                     // outputs what their rounding leaves goes along, so that weight times scale is rounded once
@@ -597,7 +607,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
             piece.slot = 1;
             if (++piece.pair == pairs) {
                 piece.pair = 0;
-                do piece.tiles = request_tiles(d, ++piece.b);
+                do piece.tiles = request_tiles(++piece.b);
                 while (piece.tiles == 0 && piece.b + 1 < d.batch);
             }
             continue;
@@ -658,7 +668,7 @@ template <typename T> __global__ void __launch_bounds__(kJoinWarps * 32) kv_join
     const KvDecodeArgs &d = a.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = d.shape.d, col = lane * 4, pairs = d.shape.hk * a.row_blocks;
     for (int64_t b = blockIdx.x; b < d.batch && blockIdx.y == 0; b += gridDim.x) {
-        if (request_tiles(d, b) > 0) continue;
+        if (request_len(d, b) > 0) continue;
         for (int e = tid; e < d.shape.hq * (D / 4); e += blockDim.x) {
             T *out = static_cast<T *>(d.out) + b * d.so.t + e / (D / 4) * d.so.h + e % (D / 4) * 4;
             *reinterpret_cast<uint2 *>(out) = make_uint2(0, 0);
@@ -666,7 +676,7 @@ template <typename T> __global__ void __launch_bounds__(kJoinWarps * 32) kv_join
         if (d.lse)
             for (int h = tid; h < d.shape.hq; h += blockDim.x) d.lse[b * d.shape.hq + h] = -INFINITY;
     }
-    if (a.by_pair && request_tiles(d, blockIdx.x / pairs) == 0) return;  // no CTA has written its entry
+    if (a.by_pair && request_len(d, blockIdx.x / pairs) == 0) return;  // no CTA has written its entry
     grid_dependency_wait();
     const int4 info = __ldcg(a.cuts + blockIdx.x);
     const int parts = info.z, b = info.w / pairs, pair = info.w - b * pairs;
@@ -746,7 +756,7 @@ struct Plan {
 };
 Plan plan(const KvDecodeArgs &d) {
     const int64_t group = d.shape.hq / d.shape.hk, pairs = d.batch * d.shape.hk * ((group + kRows - 1) / kRows);
-    const int64_t tiles = (d.max_len + kTileKeys - 1) / kTileKeys, sms = device_sm_count();
+    const int64_t tiles = (d.max_len + 31) / 32, sms = device_sm_count();
     int ranks = 1;
     while (ranks < kMaxCluster && tiles >= 2 * ranks * kWarps && pairs * 2 * ranks <= 3 * sms) ranks *= 2;
     if (tiles >= 12 * ranks * kWarps && d.batch <= kMaxFlatBatch && d.batch * (tiles + kPieceUnits) < (int64_t(1) << 30))
