@@ -88,7 +88,7 @@ qmm_status check_cache(const qmm_kv_cache *x, int64_t hk, int64_t d, KvCache &c)
     if (bytes == 0 || x->n_pages > 0x7fffffff / x->page_size) return QMM_ERR_SHAPE;
     if (x->n_pages > 0) {
         if (!x->pages) return QMM_ERR_ARG;
-        if (!aligned_to(x->pages, 16) || x->page_stride % 16) return QMM_ERR_ALIGN;
+        if (!aligned_to(x->pages, 16) || (x->n_pages > 1 && x->page_stride % 16)) return QMM_ERR_ALIGN;
         if (x->n_pages > 1 && (x->page_stride < (int64_t)bytes || x->page_stride > kMaxStride)) return QMM_ERR_SHAPE;
     }
     c.pages = static_cast<uint8_t *>(x->pages);

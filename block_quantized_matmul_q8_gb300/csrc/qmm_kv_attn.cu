@@ -201,6 +201,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
     __syncthreads();
     volatile int *abort = &abort_s;
     int stg = 0, phase = 0;  // the warp's next stage
+    bool dead = false;
 
     while (true) {
         int j0, n;  // tiles of the warp
@@ -225,6 +226,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
             j0 = int(piece.tiles * me / workers);
             n = int(piece.tiles * (me + 1) / workers) - j0;
         }
+        if (dead) n = 0;  // after a wait that gave up the other pieces are empty: the join finds its entries
         const int64_t b = piece.b;
         const int hk = piece.pair / a.row_blocks, block = piece.pair - hk * a.row_blocks;
         const int head0 = hk * a.group + block * kRows, rows = min(a.group - block * kRows, kRows);
@@ -600,7 +602,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         if (kFlat) {
             fence_proxy_async_smem();  // the partial rows' place is the ring again
             __syncthreads();
-            if (gave_up) break;
+            dead |= gave_up;
             piece.begin += units_of(piece.tiles);
             if (piece.begin >= piece.end) break;
             piece.first = 0;
@@ -680,7 +682,8 @@ template <typename T> __global__ void __launch_bounds__(kJoinWarps * 32) kv_join
     grid_dependency_wait();
     const int4 info = __ldcg(a.cuts + blockIdx.x);
     const int parts = info.z, b = info.w / pairs, pair = info.w - b * pairs;
-    if (parts == 0) return;
+    // (lengths that changed under the call would leave an entry unwritten)
+    if (parts <= 0 || info.x < 0 || parts > a.ctas - info.x || info.w < 0 || info.w >= d.batch * pairs) return;
     const int hk = pair / a.row_blocks, block = pair - hk * a.row_blocks;
     const int head0 = hk * a.group + block * kRows, rows = min(a.group - block * kRows, kRows);
     // a warp's row, and which of the row's parts: the first part is the CTA's last piece, the others are the

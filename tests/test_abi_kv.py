@@ -64,6 +64,7 @@ def bad_caches(call):
     assert call(c=C(stride=4592)) == 2                    # pages that overlap
     assert call(c=C(n=1 << 26)) == 2                      # slots past 31 bits
     assert call(c=C(data=4104)) == 4 and call(c=C(stride=4616)) == 4
+    assert call(c=C(n=1, data=4104)) == 4                 # (the stride of a single page is never taken)
 
 
 def test_append_refuses(L):

@@ -309,6 +309,31 @@ def test_decode(lens, hq, hk, d, page, qtype, dt):
     assert qmm.qmm_take_attn_error() == 0
 
 
+@pytest.mark.parametrize("lens,hq,hk,d,page,qtype,dt", [
+    ([7000, 1, 3000, 0, 31, 6999, 32, 64, 5000, 33], 8, 8, 32, 16, "q4_0", BF),
+    ([12500, 100, 0, 6400], 36, 4, 64, 32, "q4_0", FP),          # 9 heads of a kv head
+    ([25000, 0, 2000], 18, 2, 128, 256, "q8_0", BF),
+    ([0, 0, 0, 26000, 0], 4, 2, 96, 64, "q8_0", FP),
+    ([30000], 5, 1, 128, 16, "q4_0", FP),
+    ([(37 * i) % 30 for i in range(180)] + [2500, 0, 1700, 2400] + [5] * 20, 4, 4, 32, 16, "q4_0", BF),
+    ([2000 - 9 * i for i in range(200)], 4, 4, 32, 64, "q8_0", FP),
+])
+def test_decode_cut_into_parts(lens, hq, hk, d, page, qtype, dt):
+    """The tiles of all requests in one row that resident CTAs cut: few requests, many, many short ones among long
+    ones, more requests and heads than CTAs; the parts are joined in the workspace, which may hold anything."""
+    g = gen(sum(lens) + d + hq)
+    need = qmm.qmm_workspace_bytes_attn_decode_kv(len(lens), max(lens), hq, hk, d)
+    assert need > 0
+    cache, table, codes, scales = filled(g, lens, qtype, page, hk, d)
+    q = query(g, len(lens), hq, d, dt)
+    lse = torch.full((len(lens), hq), 7.0, device=DEV)
+    out = qmm.qmm_attn_decode_kv(q, cache, table, ints(lens), max_len=max(lens), lse=lse)
+    kv_ref.check_decode_kv(q, codes, scales, lens, d ** -0.5, qtype, out, lse)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    assert torch.equal(qmm.qmm_attn_decode_kv(q, cache, table, ints(lens), max_len=max(lens), workspace=ws), out)
+    assert qmm.qmm_take_attn_error() == 0
+
+
 @pytest.mark.parametrize("qtype", ["q4_0", "q8_0"])
 @pytest.mark.parametrize("dt", [BF, FP])
 @pytest.mark.parametrize("spread,kspread,scale", [(8.0, 4.0, None), (1.0, 1.0, -0.3), (1.0, 1.0, 0.0), (1e-3, 0.01, 40.0),
@@ -424,7 +449,7 @@ def test_decode_strides_streams_graphs_and_bits():
 
 
 @pytest.mark.parametrize("mode", [1, 2])
-@pytest.mark.parametrize("lens", [[100, 5], [9000], [40] * 90], ids=["short", "split", "many"])
+@pytest.mark.parametrize("lens", [[100, 5], [9000], [40] * 90, [13000, 0, 3, 20, 8000] + [1] * 20], ids=["short", "split", "many", "pieces"])
 def test_decode_waits_that_give_up(lens, mode):
     """Copies that never come (none is issued) and a wait that gives up with copies in flight: the call ends,
     reports, and the next one is right."""
@@ -437,6 +462,29 @@ def test_decode_waits_that_give_up(lens, mode):
     out = qmm.qmm_attn_decode_kv(q, cache, table, ll, max_len=max(lens))
     assert qmm.qmm_take_attn_error() == QMM_ERR_DEVICE and qmm.qmm_take_attn_error() == 0
     kv_ref.check_decode_kv(q, codes, scales, lens, 128 ** -0.5, "q8_0", out)
+
+
+def test_decode_two_workspaces_at_once():
+    """Two calls whose parts lie in workspaces of their own, on two streams, again and again."""
+    g = gen(18)
+    lens, hq, hk, d = [26000, 700, 8000], 8, 2, 64
+    cache, table, codes, scales = filled(g, lens, "q4_0", 16, hk, d)
+    need = qmm.qmm_workspace_bytes_attn_decode_kv(3, 26000, hq, hk, d)
+    assert need > 0
+    q = [query(g, 3, hq, d, BF) for _ in range(2)]
+    ll = ints(lens)
+    want = [qmm.qmm_attn_decode_kv(x, cache, table, ll, max_len=26000) for x in q]
+    ws = [torch.full((need,), 255, dtype=torch.uint8, device=DEV) for _ in q]
+    outs = [torch.empty_like(x) for x in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, o, w, s in zip(q, outs, ws, streams):
+            qmm.qmm_attn_decode_kv(x, cache, table, ll, max_len=26000, out=o, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    with pytest.raises(qmm.QMMError):
+        qmm.qmm_attn_decode_kv(q[0], cache, table, ll, max_len=26000, workspace=ws[0][:need - 256])
 
 
 def test_decode_far_pages():
