@@ -36,6 +36,8 @@ template <typename In, typename Out, bool kInterleaved, bool kQ8>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs a, int lanes_log2, int share) {
     __shared__ float2 cs[kMaxHeadDim / 2];
     __shared__ __align__(16) float rows[kWarps][256];
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();  // the attention that reads these pages may start, and waits
     const RopeArgs &p = a.rope;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t t = blockIdx.x;
@@ -175,8 +177,7 @@ template <typename In, typename Out> cudaError_t launch_append(const KvAppendArg
     const dim3 grid((unsigned)a.rope.m, (unsigned)((total + share - 1) / share));
     auto kern = a.cache.q8 ? (a.rope.interleaved ? kv_append_kernel<In, Out, true, true> : kv_append_kernel<In, Out, false, true>)
                            : (a.rope.interleaved ? kv_append_kernel<In, Out, true, false> : kv_append_kernel<In, Out, false, false>);
-    kern<<<grid, kThreads, 0, st>>>(a, lanes_log2, share);
-    return cudaGetLastError();
+    return launch_pdl(kern, grid, dim3(kThreads), 0, st, a, lanes_log2, share);
 }
 template <typename In> cudaError_t launch_append_in(const KvAppendArgs &a, qmm_float out_type, cudaStream_t st) {
     return out_type == QMM_F16 ? launch_append<In, __half>(a, st) : launch_append<In, __nv_bfloat16>(a, st);
@@ -192,6 +193,8 @@ template <typename Out, bool kQ8, int D> __global__ void __launch_bounds__(kThre
     constexpr int kItems = kReadTokens * kLanes / kThreads;  // of a thread, a head and a side
     __shared__ const uint8_t *record_s[kReadTokens];         // of the first head; null: a row that is not written
     __shared__ int token_s[kReadTokens];                     // 0..15; < 0: the page does not exist, the row is zero
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
     const int tid = threadIdx.x, log2p = a.cache.page_log2;
     const int64_t t0 = int64_t(blockIdx.x) * kReadTokens;
     if (tid < kReadTokens) {
@@ -270,12 +273,11 @@ template <typename Out, bool kQ8> cudaError_t launch_read(const KvReadArgs &a, c
     while (share > 1 && blocks * ((a.hk + share - 1) / share) < 8 * device_sm_count()) share = (share + 1) / 2;
     const dim3 grid((unsigned)blocks, (unsigned)((a.hk + share - 1) / share));
     switch (a.d) {
-        case 32: kv_read_kernel<Out, kQ8, 32><<<grid, kThreads, 0, st>>>(a, share); break;
-        case 64: kv_read_kernel<Out, kQ8, 64><<<grid, kThreads, 0, st>>>(a, share); break;
-        case 96: kv_read_kernel<Out, kQ8, 96><<<grid, kThreads, 0, st>>>(a, share); break;
-        default: kv_read_kernel<Out, kQ8, 128><<<grid, kThreads, 0, st>>>(a, share); break;
+        case 32: return launch_pdl(kv_read_kernel<Out, kQ8, 32>, grid, dim3(kThreads), 0, st, a, share);
+        case 64: return launch_pdl(kv_read_kernel<Out, kQ8, 64>, grid, dim3(kThreads), 0, st, a, share);
+        case 96: return launch_pdl(kv_read_kernel<Out, kQ8, 96>, grid, dim3(kThreads), 0, st, a, share);
+        default: return launch_pdl(kv_read_kernel<Out, kQ8, 128>, grid, dim3(kThreads), 0, st, a, share);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace

@@ -151,12 +151,13 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
     const int pairs = d.shape.hk * a.row_blocks;     // of a request
 
     const uint32_t my_ring = smem_u32(ring) + warp * ST * L::kBytes, my_full = smem_u32(full) + warp * ST * 8;
-    if (kFlat) grid_launch_dependents();  // every CTA stands at once: the join's may take the places that become free
     if (tid == 0) abort_s = 0;
     if (lane == 0) {
         for (int i = 0; i < ST; ++i) mbar_init(my_full + 8 * i, R);
         fence_mbar_init();
     }
+    grid_dependency_wait();    // the kernel before may have written anything that is read from here on
+    grid_launch_dependents();  // what follows (the join, the next call) may take the places that become free, and waits there
     Piece piece{};
     if (kFlat) {
         // each warp for itself: the sum of all units, then the request that holds the CTA's first
@@ -667,6 +668,8 @@ constexpr int kJoinWarps = 32;
 template <typename T> __global__ void __launch_bounds__(kJoinWarps * 32) kv_join_kernel(const __grid_constant__ Args a) {
     __shared__ float lse_s[kRows * kMaxParts];
     __shared__ float4 acc_s[kJoinWarps][32];
+    grid_dependency_wait();
+    grid_launch_dependents();
     const KvDecodeArgs &d = a.d;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, D = d.shape.d, col = lane * 4, pairs = d.shape.hk * a.row_blocks;
     for (int64_t b = blockIdx.x; b < d.batch && blockIdx.y == 0; b += gridDim.x) {
@@ -679,7 +682,6 @@ template <typename T> __global__ void __launch_bounds__(kJoinWarps * 32) kv_join
             for (int h = tid; h < d.shape.hq; h += blockDim.x) d.lse[b * d.shape.hq + h] = -INFINITY;
     }
     if (a.by_pair && request_len(d, blockIdx.x / pairs) == 0) return;  // no CTA has written its entry
-    grid_dependency_wait();
     const int4 info = __ldcg(a.cuts + blockIdx.x);
     const int parts = info.z, b = info.w / pairs, pair = info.w - b * pairs;
     // (lengths that changed under the call would leave an entry unwritten)
@@ -776,8 +778,7 @@ template <typename T, bool kQ8, int D> cudaError_t launch(const Args &a, Plan p,
         Args flat = a;
         flat.ctas = std::min(p.ctas, L::kCtas * device_sm_count());  // what the type and head size let stand at once
         flat.by_pair = pairs <= flat.ctas;
-        kern<<<flat.ctas, kThreads, L::kSmem, st>>>(flat);
-        e = cudaGetLastError();
+        e = launch_pdl(kern, dim3(flat.ctas), dim3(kThreads), L::kSmem, st, flat);
         if (e != cudaSuccess) return e;
         // few entries may have many parts each: a block of 32 warps for each row, else one of 8 warps for all
         const int entries = flat.by_pair ? (int)pairs : flat.ctas;
@@ -794,12 +795,14 @@ template <typename T, bool kQ8, int D> cudaError_t launch(const Args &a, Plan p,
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = L::kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = p.ranks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
