@@ -29,9 +29,9 @@ template <typename T> __device__ __forceinline__ uint4 round8(const float (&v)[8
 }
 
 // One block a token, or a share of its heads where tokens are few (as in qmm_rope.cu, whose lanes these
-// are: eight elements of a head each, four of them the partners of the other four).  Key and value
-// heads go through shared memory after the turn, so that a lane then holds eight neighbours and four
-// lanes a block of 32.
+// are: eight elements of a head each, four of them the partners of the other four).  Four lanes with
+// eight neighbours each hold a block of 32: value heads are loaded so, key heads whose partners are half a rotation apart
+// go through shared memory after the turn.
 template <typename In, typename Out, bool kInterleaved, bool kQ8>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs a, int lanes_log2, int share) {
     __shared__ float2 cs[kMaxHeadDim / 2];
@@ -53,9 +53,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
     auto load = [&](int h, float4 &x, float4 &y) {
         x = y = make_float4(0.f, 0.f, 0.f, 0.f);
         if (!live || h >= h_end) return;
-        const In *s = h < hq        ? static_cast<const In *>(p.q) + t * p.sq.t + h * p.sq.h
-                      : h < hq + hk ? static_cast<const In *>(p.k) + t * p.sk.t + (h - hq) * p.sk.h
-                                    : static_cast<const In *>(p.v) + t * p.sv.t + (h - hq - hk) * p.sv.h;
+        if (h >= hq + hk) {
+            load8<true>(static_cast<const In *>(p.v) + t * p.sv.t + (h - hq - hk) * p.sv.h, 8 * c, 8 * c + 4, x, y);
+            return;
+        }
+        const In *s = h < hq ? static_cast<const In *>(p.q) + t * p.sq.t + h * p.sq.h
+                             : static_cast<const In *>(p.k) + t * p.sk.t + (h - hq) * p.sk.h;
         load8<kInterleaved>(s, e0, e1, x, y);
     };
     int h = h_begin + warp * per_warp + sub;
@@ -109,18 +112,23 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
         if (__all_sync(0xffffffffu, is_q)) continue;
 
         // ---- keys and values: eight neighbours a lane
-        float *row = &rows[warp][sub * 8 * lanes];
-        __syncwarp();
-        if (live) {
-            *reinterpret_cast<float4 *>(row + e0) = A;
-            *reinterpret_cast<float4 *>(row + e1) = B;
+        if (!kInterleaved && __any_sync(0xffffffffu, !is_q && !is_v)) {
+            float *row = &rows[warp][sub * 8 * lanes];
+            __syncwarp();
+            if (live && !is_v) {
+                *reinterpret_cast<float4 *>(row + e0) = A;
+                *reinterpret_cast<float4 *>(row + e1) = B;
+            }
+            __syncwarp();
+            if (live && !is_v) {
+                A = *reinterpret_cast<const float4 *>(row + 8 * c);
+                B = *reinterpret_cast<const float4 *>(row + 8 * c + 4);
+            }
         }
-        __syncwarp();
-        float v[8], top = -INFINITY, low = INFINITY;
+        float v[8] = {A.x, A.y, A.z, A.w, B.x, B.y, B.z, B.w}, top = -INFINITY, low = INFINITY;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float u = live ? row[8 * c + j] : 0.f;
-            v[j] = u == u ? u : 0.f;  // NaN is held as zero, an infinity as the largest value
+            v[j] = live && v[j] == v[j] ? v[j] : 0.f;  // NaN is held as zero, an infinity as the largest value
             top = fmaxf(top, v[j]);
             low = fminf(low, v[j]);
         }
@@ -133,26 +141,21 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
         float scale = kQ8 ? fmaxf(top, -low) / 127.f : (top >= -low ? top : low) * -0.125f;
         const __half hs = __float2half_rn(fminf(fmaxf(scale, -65504.f), 65504.f));
         scale = __half2float(hs);
-        int code[8];
+        // codes as floats, and side by side as words: adding 1.5 2^23 leaves an integer in the low bits
+        uint32_t word[2] = {0, 0};
+        constexpr int kShift = kQ8 ? 8 : 4, kPer = 32 / kShift;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float q = scale == 0.f ? 0.f : rintf(__fdiv_rn(v[j], scale));
-            code[j] = int(kQ8 ? fminf(fmaxf(q, -127.f), 127.f) : fminf(fmaxf(q, -8.f), 7.f));
+            v[j] = kQ8 ? fminf(fmaxf(q, -127.f), 127.f) : fminf(fmaxf(q, -8.f), 7.f);
+            const uint32_t bits = __float_as_uint(v[j] + (12582912.f + (kQ8 ? 128.f : 8.f))) - 0x4B400000u;
+            word[j / kPer] += bits << (kShift * (j % kPer));
         }
         const int kv = h - hq - (is_v ? hk : 0);
         if (held) {
             uint8_t *side = group + (int64_t(kv) << groups_log2) * kv_record_bytes(kQ8, d) + (is_v ? kv_side_bytes(kQ8, d) : 0);
-            if (kQ8) {
-                uint32_t u[2] = {0, 0};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[j >> 2] |= uint32_t(code[j] + 128) << (8 * (j & 3));
-                *reinterpret_cast<uint2 *>(side + (c >> 1) * 256 + token * 16 + (c & 1) * 8) = make_uint2(u[0], u[1]);
-            } else {
-                uint32_t u = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u |= uint32_t(code[j] + 8) << (4 * j);
-                *reinterpret_cast<uint32_t *>(side + (c >> 2) * 256 + token * 16 + (c & 3) * 4) = u;
-            }
+            if (kQ8) *reinterpret_cast<uint2 *>(side + (c >> 1) * 256 + token * 16 + (c & 1) * 8) = make_uint2(word[0], word[1]);
+            else *reinterpret_cast<uint32_t *>(side + (c >> 2) * 256 + token * 16 + (c & 3) * 4) = word[0];
             if ((c & 3) == 0)
                 reinterpret_cast<__half *>(side + kv_scales_at(kQ8, d) + (c >> 2) * 32)[kv_scale_place(token)] = hs;
         }
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
             out += is_v ? t * p.svo.t + kv * p.svo.h : t * p.sko.t + kv * p.sko.h;
             float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = scale * float(code[j]);
+            for (int j = 0; j < 8; ++j) f[j] = scale * v[j];
             *reinterpret_cast<uint4 *>(out + 8 * c) = round8<Out>(f);
         }
     }
