@@ -186,6 +186,44 @@ template <typename In> cudaError_t launch_append_in(const KvAppendArgs &a, qmm_f
     return out_type == QMM_F16 ? launch_append<In, __half>(a, st) : launch_append<In, __nv_bfloat16>(a, st);
 }
 
+// Eight values in 16 bits, scale (fp16 bits) times code, from codes that become fp16 integers two at a time: 1024 + n
+// less 1032, (1024 + 16 n) / 16 less 72, 1024 + u less 1152, all exact.  The product is exact in fp32, and fp16's own
+// multiplication rounds it once.
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+template <typename Out> __device__ __forceinline__ uint32_t times(float scale, float x, float y) { return pack2<Out>(scale * x, scale * y); }
+template <typename Out> __device__ __forceinline__ uint4 values_q4(uint32_t x, uint16_t scale) {
+    const uint32_t y = x >> 8;
+    const __half2 less = __half2half2(__ushort_as_half(0xE408)), part = __half2half2(__ushort_as_half(0x2C00)),
+                  rest = __half2half2(__ushort_as_half(0xD480));
+    const __half2 n04 = __hadd2(as_h2((x & 0x000f000fu) | 0x64006400u), less), n15 = __hfma2(as_h2((x & 0x00f000f0u) | 0x64006400u), part, rest);
+    const __half2 n26 = __hadd2(as_h2((y & 0x000f000fu) | 0x64006400u), less), n37 = __hfma2(as_h2((y & 0x00f000f0u) | 0x64006400u), part, rest);
+    if constexpr (std::is_same<Out, __half>::value) {
+        const __half2 d = __half2half2(__ushort_as_half(scale));
+        const uint32_t a = h2bits(__hmul2(n04, d)), b = h2bits(__hmul2(n15, d)), e = h2bits(__hmul2(n26, d)), f = h2bits(__hmul2(n37, d));
+        return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(e, f, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(e, f, 0x7632));
+    } else {
+        const float d = __half2float(__ushort_as_half(scale));
+        const float2 a = __half22float2(n04), b = __half22float2(n15), e = __half22float2(n26), f = __half22float2(n37);
+        return make_uint4(times<Out>(d, a.x, b.x), times<Out>(d, e.x, f.x), times<Out>(d, a.y, b.y), times<Out>(d, e.y, f.y));
+    }
+}
+template <typename Out> __device__ __forceinline__ uint4 values_q8(uint32_t x, uint32_t y, uint16_t scale) {
+    const __half2 less = __half2half2(__ushort_as_half(0xE480));
+    const uint32_t w[2] = {x, y};
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 n = __hadd2(as_h2(__byte_perm(w[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140)), less);
+        if constexpr (std::is_same<Out, __half>::value) {
+            out[i] = h2bits(__hmul2(n, __half2half2(__ushort_as_half(scale))));
+        } else {
+            const float2 v = __half22float2(n);
+            out[i] = times<Out>(__half2float(__ushort_as_half(scale)), v.x, v.y);
+        }
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
 // Reading: a block takes kReadTokens rows of the packed output and a share of the heads.  Its first threads find
 // each row's sequence, page and record once for all heads; a lane then writes eight elements (16 bytes),
 // neighbouring lanes a whole row, and two neighbouring tokens fill the 32-byte sectors of the codes.
@@ -226,46 +264,57 @@ template <typename Out, bool kQ8, int D> __global__ void __launch_bounds__(kThre
         token_s[tid] = token;
     }
     __syncthreads();
-    const int head_step = (1 << (log2p - 4)) * kRec;
+    const int64_t head_step = int64_t(1 << (log2p - 4)) * kRec;
     const int h0 = blockIdx.y * share, h1 = min(h0 + share, a.hk);
+    // each item's codes and scale, and its places in the output
+    const uint8_t *codes[kItems], *scales[kItems];
+    Out *ko[kItems], *vo[kItems];
+    bool there[kItems];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int row = (tid + i * kThreads) / kLanes, c = (tid + i * kThreads) % kLanes, token = max(token_s[row], 0);
+        const uint8_t *p = record_s[row];
+        there[i] = p && token_s[row] >= 0;
+        codes[i] = p + h0 * head_step + (kQ8 ? (c >> 1) * 256 + (c & 1) * 8 : (c >> 2) * 256 + (c & 3) * 4) + token * 16;
+        scales[i] = p + h0 * head_step + kv_scales_at(kQ8, D) + (c >> 2) * 32 + 2 * kv_scale_place(token);
+        ko[i] = p ? static_cast<Out *>(a.ko) + (t0 + row) * a.sko.t + h0 * a.sko.h + 8 * c : nullptr;
+        vo[i] = static_cast<Out *>(a.vo) + (t0 + row) * a.svo.t + h0 * a.svo.h + 8 * c;
+    }
     for (int h = h0; h < h1; ++h) {
         uint32_t u[2][kItems][kQ8 ? 2 : 1];
-        __half s[2][kItems];
+        uint16_t s[2][kItems];
 #pragma unroll
         for (int is_v = 0; is_v < 2; ++is_v)
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int row = (tid + i * kThreads) / kLanes, c = (tid + i * kThreads) % kLanes;
-                const int token = token_s[row];
-                s[is_v][i] = __ushort_as_half(0);
                 u[is_v][i][0] = u[is_v][i][kQ8 ? 1 : 0] = 0;
-                if (!record_s[row] || token < 0) continue;
-                const uint8_t *p = record_s[row] + int64_t(h) * head_step + is_v * kSide;
+                s[is_v][i] = 0;
+                if (!there[i]) continue;
                 if constexpr (kQ8) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(p + (c >> 1) * 256 + token * 16 + (c & 1) * 8);
+                    const uint2 w = *reinterpret_cast<const uint2 *>(codes[i] + is_v * kSide);
                     u[is_v][i][0] = w.x;
                     u[is_v][i][1] = w.y;
                 } else {
-                    u[is_v][i][0] = *reinterpret_cast<const uint32_t *>(p + (c >> 2) * 256 + token * 16 + (c & 3) * 4);
+                    u[is_v][i][0] = *reinterpret_cast<const uint32_t *>(codes[i] + is_v * kSide);
                 }
-                s[is_v][i] = reinterpret_cast<const __half *>(p + kv_scales_at(kQ8, D) + (c >> 2) * 32)[kv_scale_place(token)];
+                s[is_v][i] = *reinterpret_cast<const uint16_t *>(scales[i] + is_v * kSide);
             }
 #pragma unroll
         for (int is_v = 0; is_v < 2; ++is_v)
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int row = (tid + i * kThreads) / kLanes, c = (tid + i * kThreads) % kLanes;
-                if (!record_s[row]) continue;
-                const float scale = __half2float(s[is_v][i]);
-                float f[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    f[j] = scale * float(kQ8 ? int(u[is_v][i][j >> 2] >> (8 * (j & 3)) & 255u) - 128
-                                             : int(u[is_v][i][0] >> (4 * j) & 15u) - 8);
-                Out *out = is_v ? static_cast<Out *>(a.vo) + (t0 + row) * a.svo.t + h * a.svo.h
-                                : static_cast<Out *>(a.ko) + (t0 + row) * a.sko.t + h * a.sko.h;
-                *reinterpret_cast<uint4 *>(out + 8 * c) = round8<Out>(f);
+                if (!ko[i]) continue;
+                const uint4 out = kQ8 ? values_q8<Out>(u[is_v][i][0], u[is_v][i][kQ8 ? 1 : 0], s[is_v][i])
+                                      : values_q4<Out>(u[is_v][i][0], s[is_v][i]);
+                *reinterpret_cast<uint4 *>(is_v ? vo[i] : ko[i]) = out;
             }
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+            codes[i] += head_step;
+            scales[i] += head_step;
+            if (ko[i]) ko[i] += a.sko.h;
+            vo[i] += a.svo.h;
+        }
     }
 }
 
