@@ -21,6 +21,10 @@
 // and kv head and joins through distributed shared memory, one launch.  Larger ones: the tiles of all
 // requests lie in one row that resident CTAs cut into equal parts (each scans the lengths on the device), and a second
 // launch joins the requests that were cut.  mma.sync: 8 query heads would leave tcgen05's 128 rows empty.
+//
+// 128 caches of up to 8192 tokens, 32/8 heads of 128 in 4 bits: 112 us, 5.4 TB/s (79% of the measured copy rate); 48 of
+// them 48 us; one of 131071 (40/8 heads, fp16) 39 us; one of 640 7.4 us.  About 15 us of a large call are launch, first
+// tiles and join; each further 200000 tokens take 36 us, 6.4 TB/s (94%), and in 8 bits 400000 tokens 141 us in all (91%).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
