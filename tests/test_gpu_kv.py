@@ -162,6 +162,9 @@ def test_append_extremes(qtype, src):
         assert torch.equal(codes[i], c) and torch.equal(scales[i], s)
     assert torch.equal(ko, kv_ref.values(c, s).float().to(BF)) and torch.equal(vo, ko)
     assert bool(ko.isfinite().all())
+    for dst in (BF, FP):  # read back: values below fp16's normal range, and above its largest
+        rk, rv = qmm.qmm_kv_read(cache, ints([[0]]), ints([0, 12]), 12, out_dtype=dst)
+        assert torch.equal(rk, kv_ref.values(c, s).float().to(dst)) and torch.equal(rv, rk)
 
 
 def test_append_strides_layers_and_streams():
@@ -557,6 +560,47 @@ def test_chunks_then_steps(qtype, dt):
         both = [held(i) for i in range(2)]
         kv_ref.check_decode_kv(qo, [[c[x] for c, _ in both] for x in range(2)], [[s[x] for _, s in both] for x in range(2)],
                                have, d ** -0.5, qtype, out)
+    assert qmm.qmm_take_attn_error() == 0
+
+
+def test_a_captured_step():
+    """Append and decode in one graph, replayed token after token with new inputs in the same places, against the
+    same calls made one by one on a cache of their own."""
+    hq, hk, d, page, b = 16, 4, 128, 32, 3
+    g = gen(22)
+    lens0 = [40, 1, 95]
+    cache, table, codes, scales = filled(g, lens0, "q4_0", page, hk, d, spare=6)
+    table = torch.cat((table, torch.arange(cache.pages.shape[0] - 3, cache.pages.shape[0], device=DEV, dtype=torch.int32)[:, None]), 1)
+    free = sorted(set(range(cache.pages.shape[0])) - set(table[table >= 0].tolist()))
+    for i, n in enumerate(lens0):  # the page after each sequence's last
+        table[i, -(-n // page)] = free[i]
+    other = qmm.KVPages(cache.pages.clone(), "q4_0", page, hk, d)
+    w, inv = 1 + 0.1 * normal(g, d), torch.linspace(1, 1e-3, d // 2, device=DEV)
+    qkv, slots, lens = torch.zeros(b, hq + 2 * hk, d, device=DEV), ints([0] * b), ints(lens0)
+
+    def step(where):
+        q, _, _ = qmm.qmm_kv_append(qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:], lens, inv, where, slots, w_q=w, w_k=w)
+        return qmm.qmm_attn_decode_kv(q, where, table, lens + 1, max_len=128)
+
+    def place():
+        at = lens.long()
+        slots.copy_(table[torch.arange(b, device=DEV), at // page] * page + at % page)
+
+    place()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(cache)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(cache)
+    for _ in range(20):
+        qkv.copy_(normal(g, b, hq + 2 * hk, d))
+        place()
+        graph.replay()
+        assert torch.equal(out, step(other)) and torch.equal(cache.pages, other.pages)
+        lens += 1
     assert qmm.qmm_take_attn_error() == 0
 
 
