@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "qmm_attn.cuh"
 #include "qmm_internal.h"
@@ -343,11 +344,19 @@ cudaError_t launch_kv_append(const KvAppendArgs &a, qmm_float in_type, qmm_float
     return in_type == QMM_F16 ? launch_append_in<__half>(a, out_type, st) : launch_append_in<__nv_bfloat16>(a, out_type, st);
 }
 
+namespace {
+std::atomic<bool> launched{false};  // a kernel that may report has been launched (or captured) by this process
+}
+
 cudaError_t launch_kv_read(const KvReadArgs &a, qmm_float out_type, cudaStream_t st) {
+    launched = true;
     if (a.cache.q8) return out_type == QMM_F16 ? launch_read<__half, true>(a, st) : launch_read<__nv_bfloat16, true>(a, st);
     return out_type == QMM_F16 ? launch_read<__half, false>(a, st) : launch_read<__nv_bfloat16, false>(a, st);
 }
 
-cudaError_t kv_take_error(int *code, cudaStream_t st) { return take_error(code, st); }
+cudaError_t kv_take_error(int *code, cudaStream_t st) {
+    *code = QMM_OK;
+    return launched ? take_error(code, st) : cudaSuccess;
+}
 
 }  // namespace qmm

@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "qmm_attn.cuh"
 #include "qmm_internal.h"
@@ -821,7 +822,14 @@ template <typename T, bool kQ8> cudaError_t launch_d(const Args &a, Plan p, int6
 
 }  // namespace
 
-cudaError_t kv_decode_take_error(int *code, cudaStream_t st) { return take_error(code, st); }
+namespace {
+std::atomic<bool> launched{false};  // a kernel that may report has been launched (or captured) by this process
+}
+
+cudaError_t kv_decode_take_error(int *code, cudaStream_t st) {
+    *code = QMM_OK;
+    return launched ? take_error(code, st) : cudaSuccess;
+}
 
 size_t kv_decode_workspace_bytes(const KvDecodeArgs &d) {
     const size_t ctas = plan(d).ctas, rows = ctas * 2 * kRows;
@@ -829,6 +837,7 @@ size_t kv_decode_workspace_bytes(const KvDecodeArgs &d) {
 }
 
 cudaError_t launch_kv_decode(const KvDecodeArgs &d, qmm_float t, void *ws, cudaStream_t st) {
+    launched = true;
     const Plan p = plan(d);
     Args a{};
     a.d = d;
