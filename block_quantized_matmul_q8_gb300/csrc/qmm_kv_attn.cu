@@ -17,7 +17,8 @@
 // A warp takes tiles of 32 keys (64 of small heads) on its own: a private ring of bulk copies (a record of 16 tokens is
 // contiguous), its running softmax, no barrier with other warps until the join.
 //
-// Two ways to share the work out.  Calls that fit the SMs at once: a cluster of up to 16 CTAs takes one request
+// Three ways to share the work out.  Many short requests: a warp for each request and kv head, no join.  Calls that fit
+// the SMs at once: a cluster of up to 16 CTAs takes one request
 // and kv head and joins through distributed shared memory, one launch.  Larger ones: the tiles of all
 // requests lie in one row that resident CTAs cut into equal parts (each scans the lengths on the device), and a second
 // launch joins the requests that were cut.  mma.sync: 8 query heads would leave tcgen05's 128 rows empty.
@@ -137,8 +138,11 @@ __device__ __forceinline__ void mma_more(float (&c)[4], uint32_t a0, uint32_t a1
     mma16816<__half>(c, a, b0, b1);
 }
 
-template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_bounds__(kThreads, Tile<kQ8, D>::kCtas) kv_decode_kernel(const __grid_constant__ Args a) {
+enum Form { kCluster, kFlatRow, kWarpEach };  // how the work is shared out
+
+template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_bounds__(kThreads, Tile<kQ8, D>::kCtas) kv_decode_kernel(const __grid_constant__ Args a) {
     using L = Tile<kQ8, D>;
+    constexpr bool kFlat = kForm == kFlatRow, kAlone = kForm == kWarpEach;  // kAlone: a warp has its own request and kv head
     constexpr int ST = L::kStages, NB = D / 32, kQuads = D / 4, R = L::kRecs;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kWarps * ST];
@@ -147,12 +151,13 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
     __shared__ float ml_s[kWarps][kRows][2];         // each warp's maximum and sum (log2 domain)
     __shared__ float joined_s[kRows][2];             // the CTA's
     __shared__ float weight_s[kRows][kMaxCluster];
-    __shared__ uint2 qb_s[NB][2][32];                // B fragments of two MMAs a block: k 2t, 2t + 1 and 2t + 8, 2t + 9 of head g
-    __shared__ float4 qc_s[NB][4];                   // the accumulators' first values, of heads 2t, 2t + 1
+    __shared__ uint2 qb_s[kAlone ? kWarps : 1][NB][2][32];  // B fragments of two MMAs a block: k 2t, 2t + 1 and 2t + 8, 2t + 9 of head g
+    __shared__ float4 qc_s[kAlone ? kWarps : 1][NB][4];     // the accumulators' first values, of heads 2t, 2t + 1
     const KvDecodeArgs &d = a.d;
     auto request_tiles = [&](int64_t b) { return (request_len(d, b) + L::kKeys - 1) / L::kKeys; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int rank = kFlat ? 0 : (int)cluster_rank(), ranks = kFlat ? 1 : (int)cluster_size();
+    const int rank = kForm == kCluster ? (int)cluster_rank() : 0, ranks = kForm == kCluster ? (int)cluster_size() : 1;
+    const int mine = kAlone ? warp : 0;              // of qb_s and qc_s
     const int pairs = d.shape.hk * a.row_blocks;     // of a request
 
     const uint32_t my_ring = smem_u32(ring) + warp * ST * L::kBytes, my_full = smem_u32(full) + warp * ST * 8;
@@ -199,12 +204,17 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
         piece.first = max(int(x - piece.begin) - kPieceUnits, 0);
         if (!a.by_pair && tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
     } else {
-        const int64_t at = blockIdx.x / ranks;
-        piece.b = at / pairs;
-        piece.pair = int(at - piece.b * pairs);
-        piece.tiles = request_tiles(piece.b);
+        const int64_t at = kAlone ? int64_t(blockIdx.x) * kWarps + warp : blockIdx.x / ranks;
+        if (!kAlone || at < d.batch * pairs) {
+            piece.b = at / pairs;
+            piece.pair = int(at - piece.b * pairs);
+            piece.tiles = request_tiles(piece.b);
+        } else {
+            piece.b = -1;
+        }
     }
     __syncthreads();
+    if (kAlone && piece.b < 0) return;
     volatile int *abort = &abort_s;
     int stg = 0, phase = 0;  // the warp's next stage
     bool dead = false;
@@ -226,6 +236,9 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
             }
             j0 = piece.first + int(int64_t(count) * warp / kWarps);
             n = piece.first + int(int64_t(count) * (warp + 1) / kWarps) - j0;
+        } else if (kAlone) {
+            j0 = 0;
+            n = piece.tiles;
         } else {
             if (tid == 0) piece_s = piece;
             const int64_t workers = ranks * kWarps, me = rank * kWarps + warp;
@@ -323,7 +336,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
             factor[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                if (i != warp) continue;  // a block a warp
+                if (!kAlone && i != warp) continue;  // a block a warp
                 float total = 0.f;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
@@ -332,7 +345,7 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                                         v[i][kQ8 ? 4 * m + 2 : 2 * m + 1] * (kQ8 ? times : times * 0.0625f),
                                         v[i][kQ8 ? 4 * m + 3 : 2 * m + 5] * (kQ8 ? times : times * 0.0625f)};
                     const uint2 q = make_uint2(pack2<__half>(e[0], e[1]), pack2<__half>(e[2], e[3]));
-                    qb_s[i][m][lane] = q;
+                    qb_s[mine][i][m][lane] = q;
                     const float2 y = halves(q.x), z = halves(q.y);
                     total += y.x + y.y + (kQ8 ? 1.f : 16.f) * (z.x + z.y);
                 }
@@ -340,10 +353,11 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                 total += __shfl_xor_sync(0xffffffffu, total, 2);
                 total *= (kQ8 ? -128.f : -8.f) * 0x1p-24f;
                 const float c0 = __shfl_sync(0xffffffffu, total, 8 * t), c1 = __shfl_sync(0xffffffffu, total, 8 * t + 4);
-                if (g == 0) qc_s[i][t] = make_float4(c0, c1, c0, c1);
+                if (g == 0) qc_s[mine][i][t] = make_float4(c0, c1, c0, c1);
             }
         }
-        __syncthreads();
+        if (kAlone) __syncwarp();
+        else __syncthreads();
         if (n > 0) {
             const uint32_t odd = (g & 1) ? 0x7632u : 0x5410u;  // halves of keys g and g + 8 out of four scales
             // -bias as an A operand, of rows g, g + 8, g, g + 8
@@ -379,8 +393,8 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                 uint32_t f[R][4];  // words of keys 0-7 and 8-15, of two units
 #pragma unroll
                 for (int blk = 0; blk < NB; ++blk) {
-                    const uint2 q0 = qb_s[blk][0][lane], q1 = qb_s[blk][1][lane];
-                    const float4 qc = qc_s[blk][t];
+                    const uint2 q0 = qb_s[mine][blk][0][lane], q1 = qb_s[mine][blk][1][lane];
+                    const float4 qc = qc_s[mine][blk][t];
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         const uint32_t codes = tile + r * L::kRec;
@@ -530,6 +544,31 @@ template <typename T, bool kQ8, int D, bool kFlat> __global__ void __launch_boun
                 for (int y = 4; y < 32; y <<= 1) sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], y);
             top[0] *= factor[0];
             top[1] *= factor[1];
+        }
+        if constexpr (kAlone) {  // the warp's rows are whole
+            if (n > 0 && *abort && lane == 0) atomicMax(&reported, int(QMM_ERR_DEVICE));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = 2 * t + h;
+                if (row >= rows) continue;
+                const bool none = !(sum[h] != 0.f);
+                const float inv = none ? 0.f : 1.f / sum[h];
+                T *const out = static_cast<T *>(d.out) + b * d.so.t + (head0 + row) * d.so.h;
+#pragma unroll
+                for (int blk = 0; blk < NB; ++blk) {
+                    const float lo = 0x1p24f * inv, hi = (kQ8 ? 0x1p24f : 0x1p20f) * inv;  // of rows g, of rows g + 8
+                    const uint32_t x = pack2<T>(o[2 * blk][h] * lo, o[2 * blk][2 + h] * hi);
+                    const uint32_t y = pack2<T>(o[2 * blk + 1][h] * lo, o[2 * blk + 1][2 + h] * hi);
+                    if constexpr (kQ8) {
+                        *reinterpret_cast<uint32_t *>(out + 32 * blk + 2 * g) = x;
+                        *reinterpret_cast<uint32_t *>(out + 32 * blk + 16 + 2 * g) = y;
+                    } else {
+                        *reinterpret_cast<uint2 *>(out + 32 * blk + 4 * g) = make_uint2(x, y);
+                    }
+                }
+                if (d.lse && g == 0) d.lse[b * d.shape.hq + head0 + row] = none ? -INFINITY : (top[h] + log2f(sum[h])) * kLn2;
+            }
+            return;
         }
         __syncthreads();  // the ring is free
         const bool gave_up = *abort;
@@ -755,18 +794,28 @@ template <typename T> __global__ void __launch_bounds__(kJoinWarps * 32) kv_join
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// How a call is shared out: clusters of `ranks` CTAs, or the flat form's CTAs (ranks == 0).  A cluster has a power of
-// two of them, at most one for every four tiles, three an SM in all.  The flat form pays for its cuts (about 4 us and the
-// join's launch) and wins where a warp of a cluster would get 12 tiles of the longest request or more, clusters and flat:
-// 35 requests of up to 1001, 16 heads of 64 in 8 bits (8 tiles) 14.5 and 19.7 us; 256 of 500, 32/8 heads of 128 (4)
-// 30.9 and 36.4; 1 of 12500 (6) 16.1 and 17.3, of 25000 (12) 22.7 and 21.7; 64 of 2000 (16) 26.8 and 27.2; 16 of 8000
-// (31) 40.8 and 25.8; 48 of up to 8192 (32) 83.8 and 50.4.  Its CTAs get 16 tiles at least, so that the join stays small.
+// How a call is shared out: a warp for each request and kv head (both 0), clusters of `ranks` CTAs, or the flat form's
+// CTAs (ranks == 0).
+//
+// A warp for each, four of them a CTA without any join, from one of them for every resident CTA and 8 tiles of the longest
+// request on (and where there is a single tile; no further than 64, which one warp takes about 60 us for), CTAs and
+// warps, 32/8 heads of 128: 2000 requests of 100 tokens 133.7 and 48.3 us; 256 of 30 20.7 and 7.5, of 100 22.0 and 11.5,
+// of 250 25.3 and 18.6, of 1000 (32 tiles) 43.6 and 52.4; 128 of 100 12.8 and 9.1; 64 of 30 7.0 and 5.7, of 100 7.4 and
+// 8.0; 1100 of 1000 158.9 and 130.9, of 2000 253.1 and 242.2.
+//
+// A cluster has a power of two CTAs, at most one for every four tiles, three an SM in all.  The flat form pays for its
+// cuts (about 4 us and the join's launch) and wins where a warp of a cluster would get 12 tiles of the longest request or
+// more, clusters and flat: 35 requests of up to 1001, 16 heads of 64 in 8 bits (8 tiles) 14.5 and 19.7 us; 256 of 500,
+// 32/8 heads of 128 (4) 30.9 and 36.4; 1 of 12500 (6) 16.1 and 17.3, of 25000 (12) 22.7 and 21.7; 64 of 2000 (16) 26.8
+// and 27.2; 16 of 8000 (31) 40.8 and 25.8; 48 of up to 8192 (32) 83.8 and 50.4.  Its CTAs get 16 tiles at least, so that
+// the join stays small.
 struct Plan {
     int ranks, ctas;
 };
 Plan plan(const KvDecodeArgs &d) {
     const int64_t group = d.shape.hq / d.shape.hk, pairs = d.batch * d.shape.hk * ((group + kRows - 1) / kRows);
     const int64_t tiles = (d.max_len + 31) / 32, sms = device_sm_count();
+    if (tiles == 1 || (tiles <= 64 && pairs >= kMaxCtas * sms && 8 * pairs >= kMaxCtas * sms * tiles)) return {0, 0};
     int ranks = 1;
     while (ranks < kMaxCluster && tiles >= 2 * ranks * kWarps && pairs * 2 * ranks <= 3 * sms) ranks *= 2;
     if (tiles >= 12 * ranks * kWarps && d.batch <= kMaxFlatBatch && d.batch * (tiles + kPieceUnits) < (int64_t(1) << 30))
@@ -776,9 +825,10 @@ Plan plan(const KvDecodeArgs &d) {
 
 template <typename T, bool kQ8, int D> cudaError_t launch(const Args &a, Plan p, int64_t pairs, cudaStream_t st) {
     using L = Tile<kQ8, D>;
-    auto kern = p.ranks ? kv_decode_kernel<T, kQ8, D, false> : kv_decode_kernel<T, kQ8, D, true>;
+    auto kern = p.ranks ? kv_decode_kernel<T, kQ8, D, kCluster> : p.ctas ? kv_decode_kernel<T, kQ8, D, kFlatRow> : kv_decode_kernel<T, kQ8, D, kWarpEach>;
     cudaError_t e = ensure_smem(kern, L::kSmem);
     if (e != cudaSuccess) return e;
+    if (!p.ranks && !p.ctas) return launch_pdl(kern, dim3((unsigned)((pairs + kWarps - 1) / kWarps)), dim3(kThreads), L::kSmem, st, a);
     if (!p.ranks) {
         Args flat = a;
         flat.ctas = std::min(p.ctas, L::kCtas * device_sm_count());  // what the type and head size let stand at once

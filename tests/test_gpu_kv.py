@@ -337,6 +337,30 @@ def test_decode_cut_into_parts(lens, hq, hk, d, page, qtype, dt):
     assert qmm.qmm_take_attn_error() == 0
 
 
+@pytest.mark.parametrize("lens,hq,hk,d,page,qtype,dt", [
+    ([(37 * i) % 201 for i in range(333)], 18, 2, 64, 16, "q4_0", BF),     # 9 heads of a kv head, a CTA that is not full
+    ([(91 * i) % 500 for i in range(304)] + [500], 8, 4, 128, 32, "q8_0", FP),
+    ([1 + i % 250 for i in range(700)], 3, 1, 96, 64, "q4_0", FP),
+    ([32, 0, 31, 1, 5], 6, 3, 32, 16, "q8_0", BF),                          # a single tile each
+])
+def test_decode_many_short(lens, hq, hk, d, page, qtype, dt):
+    """Many short requests, a warp for each request and kv head; one of them loses its pages."""
+    g = gen(sum(lens) + d)
+    assert qmm.qmm_workspace_bytes_attn_decode_kv(len(lens), max(lens), hq, hk, d) == 0
+    cache, table, codes, scales = filled(g, lens, qtype, page, hk, d)
+    q = query(g, len(lens), hq, d, dt)
+    lse = torch.full((len(lens), hq), 7.0, device=DEV)
+    out = qmm.qmm_attn_decode_kv(q, cache, table, ints(lens), max_len=max(lens), lse=lse)
+    kv_ref.check_decode_kv(q, codes, scales, lens, d ** -0.5, qtype, out, lse)
+    assert torch.equal(qmm.qmm_attn_decode_kv(q, cache, table, ints(lens), max_len=max(lens)), out)
+    assert qmm.qmm_take_attn_error() == 0
+    bad = table.clone()
+    bad[2] = cache.pages.shape[0]
+    again = qmm.qmm_attn_decode_kv(q, cache, bad, ints(lens), max_len=max(lens))
+    rest = torch.arange(len(lens), device=DEV) != 2
+    assert not again[2].any() and torch.equal(again[rest], out[rest]) and qmm.qmm_take_attn_error() == QMM_ERR_IDS
+
+
 @pytest.mark.parametrize("qtype", ["q4_0", "q8_0"])
 @pytest.mark.parametrize("dt", [BF, FP])
 @pytest.mark.parametrize("spread,kspread,scale", [(8.0, 4.0, None), (1.0, 1.0, -0.3), (1.0, 1.0, 0.0), (1e-3, 0.01, 40.0),
@@ -452,7 +476,8 @@ def test_decode_strides_streams_graphs_and_bits():
 
 
 @pytest.mark.parametrize("mode", [1, 2])
-@pytest.mark.parametrize("lens", [[100, 5], [9000], [40] * 90, [13000, 0, 3, 20, 8000] + [1] * 20], ids=["short", "split", "many", "pieces"])
+@pytest.mark.parametrize("lens", [[100, 5], [9000], [40] * 90, [13000, 0, 3, 20, 8000] + [1] * 20, [60] * 400],
+                         ids=["short", "split", "many", "pieces", "alone"])
 def test_decode_waits_that_give_up(lens, mode):
     """Copies that never come (none is issued) and a wait that gives up with copies in flight: the call ends,
     reports, and the next one is right."""
