@@ -52,7 +52,9 @@ constexpr int kMaxFlatBatch = 1024, kMaxParts = 1024;
 constexpr int kMaxCtas = 4;      // of one SM
 constexpr int kPieceUnits = 12;  // what a piece costs beside its tiles, in tiles (128 caches of up to 8192: 114.9 us
                                  // with 8, 111.8 with 12; 256 of up to 2000: 71.9 and 69.1; 48 of 8192 even)
-
+constexpr int kMinUnits = 4;     // units of a CTA at least, a tile for each warp (with max_len 131072, one request of 100
+                                 // tokens: 9.0 us with 1, 6.2 with 4, 8.9 with 13; of 640 9.4, 8.9 and 11.2; of 4000
+                                 // 10.7, 10.5 and 11.7; 4 of 1000 among 64 places of up to 8192 11.1, 12.0 and 13.1)
 template <bool kQ8, int D> struct Tile {
     static constexpr int kSide = kv_side_bytes(kQ8, D), kScales = kv_scales_at(kQ8, D);
     static constexpr int kRec = kv_record_bytes(kQ8, D);
@@ -92,7 +94,12 @@ __device__ __forceinline__ int request_len(const KvDecodeArgs &d, int64_t b) {
     return (int)min(max(int64_t(d.lens[b]), int64_t(0)), d.max_len);
 }
 // The flat form's row has kPieceUnits units and one for each tile for every request and kv head, so that
-// a CTA of many short pieces gets fewer tiles.  CTA c takes the units [total c / ctas, total (c + 1) / ctas) of it.
+// a CTA of many short pieces gets fewer tiles.  CTA c of those that take part takes the units [total c / ctas,
+// total (c + 1) / ctas) of it.  The grid is made for requests of max_len; where the lengths turn out to hold fewer than kMinUnits
+// units a CTA, fewer CTAs take part: none is without a unit, so every part that the join counts has been written.
+__device__ __forceinline__ int taking_part(int64_t total, int ctas) {
+    return (int)min(int64_t(ctas), max(total / kMinUnits, int64_t(1)));
+}
 __device__ __forceinline__ int64_t cut(int64_t total, int c, int ctas) { return total * c / ctas; }
 __device__ __forceinline__ int cta_of(int64_t total, int64_t unit, int ctas) { return int(((unit + 1) * ctas - 1) / total); }
 __device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + kPieceUnits : 0; }
@@ -175,7 +182,11 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
         for (int i = lane; i < d.batch; i += 32) sum += units_of(request_tiles(i));
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        const int64_t total = int64_t(sum) * pairs, x = cut(total, blockIdx.x, a.ctas);
+        const int64_t total = int64_t(sum) * pairs;
+        const int ctas = taking_part(total, a.ctas);
+        if (!a.by_pair && tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (int(blockIdx.x) >= ctas) return;
+        const int64_t x = cut(total, blockIdx.x, ctas);
         int before = 0, units = kPieceUnits;  // of one head of the requests before the piece's, of that
         for (int base = 0; base < d.batch; base += 32) {
             const int own = base + lane < d.batch ? units_of(request_tiles(base + lane)) : 0;
@@ -196,13 +207,12 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
             before += __shfl_sync(0xffffffffu, upto, 31);
         }
         piece.total = total;
-        piece.end = cut(total, blockIdx.x + 1, a.ctas);
+        piece.end = cut(total, blockIdx.x + 1, ctas);
         piece.tiles = units - kPieceUnits;
         piece.begin = int64_t(before) * pairs;
         piece.pair = int((x - piece.begin) / units);
         piece.begin += int64_t(piece.pair) * units;
         piece.first = max(int(x - piece.begin) - kPieceUnits, 0);
-        if (!a.by_pair && tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
     } else {
         const int64_t at = kAlone ? int64_t(blockIdx.x) * kWarps + warp : blockIdx.x / ranks;
         if (!kAlone || at < d.batch * pairs) {
@@ -229,7 +239,7 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
                 piece_s = piece;
                 if (piece.first == 0 && (!piece.whole || a.by_pair)) {
                     const int64_t place = piece.b * pairs + piece.pair;
-                    const int last = cta_of(piece.total, piece.begin + units_of(piece.tiles) - 1, a.ctas);
+                    const int last = cta_of(piece.total, piece.begin + units_of(piece.tiles) - 1, taking_part(piece.total, a.ctas));
                     a.cuts[a.by_pair ? place : blockIdx.x] =
                         make_int4(int(blockIdx.x), piece.slot, piece.whole ? 0 : last - int(blockIdx.x) + 1, int(place));
                 }
