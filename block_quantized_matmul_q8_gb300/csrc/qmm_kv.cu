@@ -292,7 +292,7 @@ template <typename Out, bool kQ8, int D> __global__ void __launch_bounds__(kThre
         for (int is_v = 0; is_v < 2; ++is_v)
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                u[is_v][i][0] = u[is_v][i][kQ8 ? 1 : 0] = 0;
+                u[is_v][i][0] = u[is_v][i][kQ8 ? 1 : 0] = kQ8 ? 0x80808080u : 0x88888888u;  // code 0: a row of no page is +0
                 s[is_v][i] = 0;
                 if (!there[i]) continue;
                 if constexpr (kQ8) {
