@@ -237,8 +237,8 @@ constexpr int kReadTokens = 32;
 template <typename Out, bool kQ8, int D> __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadArgs a, int share) {
     constexpr int kRec = kv_record_bytes(kQ8, D), kSide = kv_side_bytes(kQ8, D), kLanes = D / 8;
     constexpr int kItems = kReadTokens * kLanes / kThreads;  // of a thread, a head and a side
-    __shared__ const uint8_t *record_s[kReadTokens];         // of the first head; null: a row that is not written
-    __shared__ int token_s[kReadTokens];                     // 0..15; < 0: the page does not exist, the row is zero
+    __shared__ const uint8_t *record_s[kReadTokens];         // of the first head
+    __shared__ int token_s[kReadTokens];                     // 0..15; -1: the page does not exist, the row is zero; -2: it is not written
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int tid = threadIdx.x, log2p = a.cache.page_log2;
@@ -246,7 +246,7 @@ template <typename Out, bool kQ8, int D> __global__ void __launch_bounds__(kThre
     if (tid < kReadTokens) {
         const int64_t t = t0 + tid;
         const uint8_t *record = nullptr;
-        int token = 0;
+        int token = -2;
         if (t < a.tokens) {
             int64_t lo = 0, hi = a.n_seqs;  // the last sequence that starts at or before t
             while (hi - lo > 1) {
@@ -279,10 +279,10 @@ template <typename Out, bool kQ8, int D> __global__ void __launch_bounds__(kThre
     for (int i = 0; i < kItems; ++i) {
         const int row = (tid + i * kThreads) / kLanes, c = (tid + i * kThreads) % kLanes, token = max(token_s[row], 0);
         const uint8_t *p = record_s[row];
-        there[i] = p && token_s[row] >= 0;
+        there[i] = token_s[row] >= 0;
         codes[i] = p + h0 * head_step + (kQ8 ? (c >> 1) * 256 + (c & 1) * 8 : (c >> 2) * 256 + (c & 3) * 4) + token * 16;
         scales[i] = p + h0 * head_step + kv_scales_at(kQ8, D) + (c >> 2) * 32 + 2 * kv_scale_place(token);
-        ko[i] = p ? static_cast<Out *>(a.ko) + (t0 + row) * a.sko.t + h0 * a.sko.h + 8 * c : nullptr;
+        ko[i] = token_s[row] > -2 ? static_cast<Out *>(a.ko) + (t0 + row) * a.sko.t + h0 * a.sko.h + 8 * c : nullptr;
         vo[i] = static_cast<Out *>(a.vo) + (t0 + row) * a.svo.t + h0 * a.svo.h + 8 * c;
     }
     for (int h = h0; h < h1; ++h) {
