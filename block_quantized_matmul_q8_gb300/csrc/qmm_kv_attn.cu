@@ -8,8 +8,10 @@
 //     2^-24 with the query's elements divided by 16): one operation for two codes.  The bias is the accumulator's first
 //     value, -bias sum q of the block, and the block's scale multiplies the fp32 accumulator.  Queries
 //     are scaled by a power of two to fp16's upper range, where 16-bit inputs are exact down to 2^-14 of a head's largest.
-//   - values: the block's scale multiplies the weights, p d_jb rounded to fp16 (11 bits; below
-//     2^-14 an absolute 2^-25); codes enter as subnormals too, and a second MMA adds -bias times the same weights
+//   - values: the block's scale multiplies the weights, p d_jb rounded to fp16 (11 bits). The weights are p 2^15 until
+//     a value scale of 2 or more comes, then p 2^(15 - E) for scales from 2^E on: the products stay within fp16, and what
+//     they lose below its normal range is 2^-40 (times a code) or, where scales are large, 2^-40 of the largest of them.
+//     Codes enter as subnormals too, and a second MMA adds -bias times the same weights
 //     to the same fp32 sums, at once, so that the sums stay as small as the output.
 //   - keys are the MMA's 16 rows and query heads its 8 columns, so that no row is empty; the weights reach the
 //     second product's layout by movmatrix.  Codes come by ldmatrix with neighbouring codes in one 16-bit unit,
@@ -115,6 +117,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ float2 halves(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
 __device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
     return h2bits(__hmul2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y)));
@@ -122,6 +129,22 @@ __device__ __forceinline__ uint32_t mul2(uint32_t x, uint32_t y) {
 __device__ __forceinline__ uint32_t fma2(uint32_t x, uint32_t y, uint32_t z) {
     return h2bits(__hfma2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y),
                           *reinterpret_cast<const __half2 *>(&z)));
+}
+// Two floats at a time
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+    float2 y;
+    asm("{.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;}"
+        : "=f"(y.x), "=f"(y.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return y;
+}
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+    float2 y;
+    asm("{.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\n"
+        "fma.rn.f32x2 x, x, y, z;\nmov.b64 {%0, %1}, x;}"
+        : "=f"(y.x), "=f"(y.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return y;
 }
 // Two 16-bit values of a word
 template <typename T> __device__ __forceinline__ float2 values(uint32_t x) {
@@ -320,6 +343,8 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
 
         // the warp's running softmax of heads 2 t, 2 t + 1: its keys are those of lanes with the same t
         float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, o[D / 16][4];
+        float up_w = 15.f;               // weights are p 2^up_w, and so are their sum and o
+        float out_unit = 0x1p24f;        // of o's columns that hold codes as they are
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float factor[2];  // of heads 2t, 2t + 1
@@ -449,13 +474,28 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
 #pragma unroll
                     for (int r = 1; r < R; ++r) m[h] = fmaxf(m[h], fmaxf(s[r][h], s[r][2 + h]));
                 }
-                if (__any_sync(0xffffffffu, m[0] > top[0] || m[1] > top[1])) {
+                // the tile's value scales, two or four a lane: is one of them 2 or more?
+                constexpr int kScaleWords = R * NB * 8, kPerLane = (kScaleWords + 31) / 32;
+                uint2 vs = make_uint2(0, 0);
+                if (lane * kPerLane < kScaleWords) {
+                    const int rec = lane * kPerLane / (NB * 8), at = lane * kPerLane % (NB * 8);
+                    const uint32_t from = tile + rec * L::kRec + L::kSide + L::kScales + at * 4;
+                    if constexpr (kPerLane == 2) vs = lds64(from);
+                    else vs.x = lds32(from);
+                }
+                const bool large = ((vs.x | vs.y) & 0x40004000u) != 0;
+                if (__any_sync(0xffffffffu, large || m[0] > top[0] || m[1] > top[1])) {
+                    const float before = up_w;
+                    if (__any_sync(0xffffffffu, large)) {  // fp16 bits of the largest; their exponent is 15 for 1
+                        const uint32_t most = max(max(vs.x & 0x7fffu, vs.x >> 16 & 0x7fffu), max(vs.y & 0x7fffu, vs.y >> 16 & 0x7fffu));
+                        up_w = fminf(up_w, 30.f - float(__reduce_max_sync(0xffffffffu, most) >> 10));
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
 #pragma unroll
                         for (int y = 4; y < 32; y <<= 1) m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], y));
                         const float now = fmaxf(top[h], m[h]);
-                        const float f = top[h] == -INFINITY ? 1.f : ex2((top[h] - now) * factor[h]);
+                        const float f = top[h] == -INFINITY ? 1.f : ex2(fmaf(top[h] - now, factor[h], up_w - before));
                         top[h] = now;
                         sum[h] *= f;
 #pragma unroll
@@ -465,14 +505,17 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
                         }
                     }
                 }
+                const float2 base = make_float2(top[0] == -INFINITY ? 0.f : -top[0], top[1] == -INFINITY ? 0.f : -top[1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float base = top[h] == -INFINITY ? 0.f : top[h] * factor[h];
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-                    for (int r = 0; r < R; ++r)
-#pragma unroll
-                        for (int e = h; e < 4; e += 2) s[r][e] = ex2(fmaf(s[r][e], factor[h], -base));
-                }
+                    for (int e = 0; e < 4; e += 2) {
+                        // the difference first: the largest weight is 2^up_w exactly, and no other is larger
+                        const float2 x = fma_f32x2(add_f32x2(make_float2(s[r][e], s[r][e + 1]), base), make_float2(factor[0], factor[1]),
+                                                   make_float2(up_w, up_w));
+                        s[r][e] = ex2(x.x);
+                        s[r][e + 1] = ex2(x.y);
+                    }
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -554,6 +597,10 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
                 for (int y = 4; y < 32; y <<= 1) sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], y);
             top[0] *= factor[0];
             top[1] *= factor[1];
+            const float down = ex2(-up_w);
+            sum[0] *= down;
+            sum[1] *= down;
+            out_unit *= down;
         }
         if constexpr (kAlone) {  // the warp's rows are whole
             if (n > 0 && *abort && lane == 0) atomicMax(&reported, int(QMM_ERR_DEVICE));
@@ -566,7 +613,7 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
                 T *const out = static_cast<T *>(d.out) + b * d.so.t + (head0 + row) * d.so.h;
 #pragma unroll
                 for (int blk = 0; blk < NB; ++blk) {
-                    const float lo = 0x1p24f * inv, hi = (kQ8 ? 0x1p24f : 0x1p20f) * inv;  // of rows g, of rows g + 8
+                    const float lo = out_unit * inv, hi = (kQ8 ? out_unit : out_unit * 0.0625f) * inv;  // of rows g, of rows g + 8
                     const uint32_t x = pack2<T>(o[2 * blk][h] * lo, o[2 * blk][2 + h] * hi);
                     const uint32_t y = pack2<T>(o[2 * blk + 1][h] * lo, o[2 * blk + 1][2 + h] * hi);
                     if constexpr (kQ8) {
@@ -594,7 +641,7 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
             if (row >= to_rows) continue;
 #pragma unroll
             for (int blk = 0; blk < NB; ++blk) {
-                constexpr float lo = 0x1p24f, hi = kQ8 ? 0x1p24f : 0x1p20f;  // of rows g, of rows g + 8
+                const float lo = out_unit, hi = kQ8 ? out_unit : out_unit * 0.0625f;  // of rows g, of rows g + 8
                 const float e[4] = {o[2 * blk][h] * lo, o[2 * blk][2 + h] * hi, o[2 * blk + 1][h] * lo, o[2 * blk + 1][2 + h] * hi};
                 if constexpr (kQ8) {
                     *reinterpret_cast<float2 *>(dst + 32 * blk + 2 * g) = make_float2(e[0], e[1]);

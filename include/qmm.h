@@ -536,10 +536,13 @@ QMM_API qmm_status qmm_kv_read(const qmm_kv_cache *cache, const int32_t *table, 
  * qmm_take_attn_error says QMM_ERR_IDS.  Heads as for qmm_attn_prompt, head_dim a multiple of 32.
  * The same inputs on the same GPU give the same bits.  Accuracy, with u = 2^-8 (bf16) or 2^-11 (f16),
  * v_j = d_j code_j and exact the formula's value on what the cache stands for:
- * |out - exact| <= u |out| + (w + e) sum_j p_j |v_j| + 2^-25 sum_j (|v_j| + |code_j|) / sum_j exp(s_j - max s):
+ * |out - exact| <= u |out| + (w + e) sum_j p_j |v_j| + c sum_j p_j |d_j|
+ *                  + r 2^-24 sum_j (|v_j| + |code_j|) / sum_j exp(s_j - max s):
  * the product of weight and value scale is rounded to fp16, in bf16 the weight before it too, so w is 2^-10
- * (bf16) or 2^-11 (f16); the last term is what weights and products below fp16's normal range lose; e is that of
- * qmm_attn_prompt with sum_d |q_d k_jd| replaced by 23 (Q4_0) or 383 (Q8_0) times sum over blocks of |d| sum_d |q_d|.
+ * (bf16) or 2^-11 (f16); c, 2^-13 (Q4_0) or 2^-12 (Q8_0) of a step between codes, is the rounding of sums that the codes enter
+ * with their bias; the last term is what weights and products below fp16's normal range lose, r being 2^-15 times the
+ * larger of 1 and the largest value scale; e is that of qmm_attn_prompt with sum_d |q_d k_jd| replaced by 23 (Q4_0)
+ * or 383 (Q8_0) times sum over blocks of |d| sum_d |q_d|.
  */
 QMM_API size_t qmm_workspace_bytes_attn_decode_kv(int64_t batch, int64_t max_len, int64_t heads_q, int64_t heads_kv,
                                                   int64_t head_dim);
