@@ -183,6 +183,7 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
     __shared__ float weight_s[kRows][kMaxCluster];
     __shared__ uint2 qb_s[kAlone ? kWarps : 1][NB][2][32];  // B fragments of two MMAs a block: k 2t, 2t + 1 and 2t + 8, 2t + 9 of head g
     __shared__ float4 qc_s[kAlone ? kWarps : 1][NB][4];     // the accumulators' first values, of heads 2t, 2t + 1
+    __shared__ float beyond_s[kWarps][kRows];               // what a head's factor from sums to scores has beyond 2^127
     const KvDecodeArgs &d = a.d;
     auto request_tiles = [&](int64_t b) { return (request_len(d, b) + L::kKeys - 1) / L::kKeys; };
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -362,11 +363,14 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
             }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            // times 2^up: the largest element into [2^13, 2^14); a negative scale turns the queries
-            const int up = most > 0.f ? max(-100, min(100, 140 - int(__float_as_uint(most) >> 23))) : 0;
+            // times 2^up: the largest element into [2^13, 2^14), -115 at least; a negative scale turns the queries
+            const int up = most > 0.f ? min(100, 140 - int(__float_as_uint(most) >> 23)) : 0;
             const float times = copysignf(__int_as_float((127 + up) << 23), a.scale_log2);
-            // not zero, so that a score of minus infinity stays one
-            const float f = fmaxf(fabsf(a.scale_log2) * __int_as_float((127 + 12 - up / 2) << 23) * __int_as_float((127 + 12 - (up - up / 2)) << 23), 1e-37f);
+            // Not zero, so that a score of minus infinity stays one; 2^127 at most, so that a difference of zero stays one: any
+            // other is then far beyond what leaves a weight, and only the scores' maximum takes what lies beyond
+            const float f0 = fabsf(a.scale_log2) * __int_as_float((127 + 12 - up / 2) << 23), f1 = __int_as_float((127 + 12 - (up - up / 2)) << 23);
+            const float f = fminf(fmaxf(f0 * f1, 1e-37f), 0x1p127f);
+            beyond_s[warp][g] = fmaxf(f0 * (f1 * 0x1p-127f), 1.f);
             factor[0] = __shfl_sync(0xffffffffu, f, 8 * t);
             factor[1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
@@ -595,8 +599,8 @@ template <typename T, bool kQ8, int D, Form kForm> __global__ void __launch_boun
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int y = 4; y < 32; y <<= 1) sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], y);
-            top[0] *= factor[0];
-            top[1] *= factor[1];
+            top[0] = top[0] * factor[0] * beyond_s[warp][2 * t];
+            top[1] = top[1] * factor[1] * beyond_s[warp][2 * t + 1];
             const float down = ex2(-up_w);
             sum[0] *= down;
             sum[1] *= down;

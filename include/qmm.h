@@ -533,7 +533,8 @@ QMM_API qmm_status qmm_kv_read(const qmm_kv_cache *cache, const int32_t *table, 
  *             NULL when that is 0.
  * A request without tokens gives zeros (lse -infinity).  Cache places past lens[b] have no influence,
  * whatever they hold.  The tokens of a page outside [0, n_pages) count as not there, and
- * qmm_take_attn_error says QMM_ERR_IDS.  Heads as for qmm_attn_prompt, head_dim a multiple of 32.
+ * qmm_take_attn_error says QMM_ERR_IDS.  Heads as for qmm_attn_prompt, head_dim a multiple of 32.  Scores stay within
+ * fp32 (2^127); an infinity or a NaN in a query makes its head's row NaN (lse too) and no other.
  * The same inputs on the same GPU give the same bits.  Accuracy, with u = 2^-8 (bf16) or 2^-11 (f16),
  * v_j = d_j code_j and exact the formula's value on what the cache stands for:
  * |out - exact| <= u |out| + (w + e) sum_j p_j |v_j| + c sum_j p_j |d_j|
