@@ -11,7 +11,7 @@
 //
 // Both move each byte once.  8192 tokens of 32 + 8 + 8 fp32 heads of 128, with the values: 62.3 us, 5.0 TB/s (74% of the
 // measured copy rate; issue slots 70% busy: a third of the heads are quantized); 2048 tokens 19.7 us, 6 of them start
-// and end; one token 4.3.  131072 tokens of 8 heads of 128 read back: 110.8 us, 6.2 TB/s (92%); 32768 31.6 us.
+// and end; one token 4.3.  131072 tokens of 8 heads of 128 read back: 110.8 us, 6.2 TB/s (92%); 32768 31.9 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -25,9 +25,12 @@
 // requests lie in one row that resident CTAs cut into equal parts (each scans the lengths on the device), and a second
 // launch joins the requests that were cut.  mma.sync: 8 query heads would leave tcgen05's 128 rows empty.
 //
-// 128 caches of up to 8192 tokens, 32/8 heads of 128 in 4 bits: 112 us, 5.4 TB/s (79% of the measured copy rate); 48 of
-// them 48 us; one of 131071 (40/8 heads, fp16) 39 us; one of 640 7.4 us.  About 15 us of a large call are launch, first
+// 128 caches of up to 8192 tokens, 32/8 heads of 128 in 4 bits: 114 us, 5.3 TB/s (78% of the measured copy rate); 48 of
+// them 49 us; one of 131071 (40/8 heads, fp16) 40 us; one of 640 7.5 us.  About 15 us of a large call are launch, first
 // tiles and join; each further 200000 tokens take 36 us, 6.4 TB/s (94%), and in 8 bits 400000 tokens 141 us in all (91%).
+// Value scales of 2 and more, where every tile looks for the largest, cost 7 to 10%.  More than 8 query heads of a kv head
+// are blocks of 8 that each copy and unpack the records again: 131071 tokens of 2 kv heads of 128 take 20.8 us with 16
+// query heads, 24.0 with 32, 34.4 with 64 (floor 5.6), of one kv head with 128 query heads 57.4 (floor 2.8).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -869,7 +872,8 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // more, clusters and flat: 35 requests of up to 1001, 16 heads of 64 in 8 bits (8 tiles) 14.5 and 19.7 us; 256 of 500,
 // 32/8 heads of 128 (4) 30.9 and 36.4; 1 of 12500 (6) 16.1 and 17.3, of 25000 (12) 22.7 and 21.7; 64 of 2000 (16) 26.8
 // and 27.2; 16 of 8000 (31) 40.8 and 25.8; 48 of up to 8192 (32) 83.8 and 50.4.  Its CTAs get 16 tiles at least, so that
-// the join stays small.
+// the join stays small.  Beyond 1024 requests, whose lengths each warp would scan, there is no flat form: one long request
+// among them is one CTA's or cluster's work (1000 requests of 100 tokens and one of 65536 107 us, 1100 and one 523).
 struct Plan {
     int ranks, ctas;
 };
